@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libgqa_paged.so")
 GQA_OK = 0
 GQA_KV_BF16 = 0
 GQA_KV_FP8_E4M3 = 1
+GQA_KV_FP4 = 2
 GQA_MAX_SPLITS = 64
 GQA_SPLITS_BALANCED = -1
 
@@ -28,6 +29,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_L = ctypes.c_int64
 
 # name -> (restype, argtypes); the exported symbols of include/gqa_paged.h
 SIGNATURES = {
@@ -56,6 +58,10 @@ SIGNATURES = {
     "gqa_paged_gather": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P]),
     "gqa_paged_append_kv": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I,
                                  _P, _P]),
+    "gqa_paged_write_kv": (_I, [_P, _P, _L, _L, _P, _P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _I,
+                                _I, _I, _I, _I, _P, _P]),
+    "gqa_paged_read_kv": (_I, [_P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _L,
+                               _I, _P, _P, _P, _P]),
     "gqa_paged_append_decode": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _I,
                                      _I, _I, _I, ctypes.c_float, _I, _I, _P, _P, _P, _SZ, _P]),
     "gqa_get_error": (_I, [_P, _P]),
@@ -125,8 +131,35 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
 _KV_DTYPES = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
 
 
-def _kv_code(t: torch.Tensor) -> int:
-    return GQA_KV_BF16 if t.dtype == torch.bfloat16 else GQA_KV_FP8_E4M3
+# Bytes of a token's row in a 4-bit pool, 9 * head_dim / 16 -> head_dim.  No e4m3 pool has rows
+# of these widths, so the last dimension tells the two uint8 pools apart.
+_FP4_ROWS = {36: 64, 72: 128}
+
+
+def _kv_layout(t: torch.Tensor) -> Tuple[int, int]:
+    """(kv_dtype code, head_dim) of a pool [num_pages][Hk][P][row]."""
+    if t.dim() != 4:
+        raise ValueError("KV pools must be [num_pages][Hk][page_size][row]")
+    row = t.shape[3]
+    if t.dtype == torch.bfloat16:
+        return GQA_KV_BF16, row
+    if t.dtype == torch.uint8 and row in _FP4_ROWS:
+        return GQA_KV_FP4, _FP4_ROWS[row]
+    return GQA_KV_FP8_E4M3, row
+
+
+def _need_scales(kv_dtype: int, num_pages: int, Hk: int, k_scale, v_scale):
+    """e4m3 pools need scales [num_pages][Hk]; 4-bit pools take factors [Hk] or None."""
+    if kv_dtype == GQA_KV_FP8_E4M3:
+        if k_scale is None or v_scale is None:
+            raise ValueError("fp8 KV needs k_scale and v_scale")
+        _need(k_scale, "k_scale", torch.float32, (num_pages, Hk))
+        _need(v_scale, "v_scale", torch.float32, (num_pages, Hk))
+    elif kv_dtype == GQA_KV_FP4:
+        if k_scale is not None:
+            _need(k_scale, "k_scale", torch.float32, (Hk,))
+        if v_scale is not None:
+            _need(v_scale, "v_scale", torch.float32, (Hk,))
 
 
 # ------------------------------------------------------------------------ raw ABI names
@@ -166,25 +199,22 @@ def gqa_paged_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
                      workspace: Optional[torch.Tensor] = None, want_lse: bool = True,
                      stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Paged GQA decode.  q bf16 [B][Hq][D]; pools [num_pages][Hk][P][D] bf16 or e4m3
-    (uint8/float8_e4m3fn with fp32 scales [num_pages][Hk]); page_table int32 [B][pt_stride];
+    (uint8/float8_e4m3fn with fp32 scales [num_pages][Hk]), or 4-bit (new_fp4_pool; optional
+    fp32 factors [Hk] as k_scale / v_scale); page_table int32 [B][pt_stride];
     seq_lens int32 [B].  Returns (out bf16 [B][Hq][D], lse fp32 [B][Hq] or None)."""
     _need(q, "q", torch.bfloat16)
     B, Hq, D = q.shape
     _need(k_pages, "k_pages", _KV_DTYPES)
     _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
-    num_pages, Hk, P, D2 = k_pages.shape
+    kv_dtype, D2 = _kv_layout(k_pages)
+    num_pages, Hk, P, _ = k_pages.shape
     if D2 != D:
         raise ValueError("head_dim of q and the KV pools differ")
     _need(page_table, "page_table", torch.int32)
     _need(seq_lens, "seq_lens", torch.int32, (B,))
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B][pt_stride]")
-    kv_dtype = _kv_code(k_pages)
-    if kv_dtype == GQA_KV_FP8_E4M3:
-        if k_scale is None or v_scale is None:
-            raise ValueError("fp8 KV needs k_scale and v_scale")
-        _need(k_scale, "k_scale", torch.float32, (num_pages, Hk))
-        _need(v_scale, "v_scale", torch.float32, (num_pages, Hk))
+    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
     pt_stride = page_table.shape[1]
     if out is None:
         out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=q.device)
@@ -222,19 +252,15 @@ def gqa_paged_decode_partial(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
     B, Hq, D = q.shape
     _need(k_pages, "k_pages", _KV_DTYPES)
     _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
-    num_pages, Hk, P, D2 = k_pages.shape
+    kv_dtype, D2 = _kv_layout(k_pages)
+    num_pages, Hk, P, _ = k_pages.shape
     if D2 != D:
         raise ValueError("head_dim of q and the KV pools differ")
     _need(page_table, "page_table", torch.int32)
     _need(seq_lens, "seq_lens", torch.int32, (B,))
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B][pt_stride]")
-    kv_dtype = _kv_code(k_pages)
-    if kv_dtype == GQA_KV_FP8_E4M3:
-        if k_scale is None or v_scale is None:
-            raise ValueError("fp8 KV needs k_scale and v_scale")
-        _need(k_scale, "k_scale", torch.float32, (num_pages, Hk))
-        _need(v_scale, "v_scale", torch.float32, (num_pages, Hk))
+    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
     pt_stride = page_table.shape[1]
     if o_part is None:
         o_part = torch.empty(B, Hq, D, dtype=torch.float32, device=q.device)
@@ -271,10 +297,14 @@ def gqa_paged_decode_static_scratch(q: torch.Tensor, k_pages: torch.Tensor,
     B, Hq, D = q.shape
     _need(k_pages, "k_pages", _KV_DTYPES)
     _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
+    kv_dtype, D2 = _kv_layout(k_pages)
     num_pages, Hk, P, _ = k_pages.shape
+    if D2 != D:
+        raise ValueError("head_dim of q and the KV pools differ")
     _need(page_table, "page_table", torch.int32)
     _need(seq_lens, "seq_lens", torch.int32, (B,))
-    kv_dtype = _kv_code(k_pages)
+    if kv_dtype == GQA_KV_FP4:
+        _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
     if out is None:
         out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=q.device)
     if lse is None:
@@ -293,7 +323,8 @@ def gqa_paged_decode_static_scratch(q: torch.Tensor, k_pages: torch.Tensor,
 def _append_args(k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale):
     _need(k_pages, "k_pages", _KV_DTYPES)
     _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
-    num_pages, Hk, P, D = k_pages.shape
+    kv_dtype, D = _kv_layout(k_pages)
+    num_pages, Hk, P, _ = k_pages.shape
     _need(seq_lens, "seq_lens", torch.int32)
     B = seq_lens.shape[0]
     _need(k_new, "k_new", torch.bfloat16, (B, Hk, D))
@@ -301,12 +332,7 @@ def _append_args(k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, 
     _need(page_table, "page_table", torch.int32)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B][pt_stride]")
-    kv_dtype = _kv_code(k_pages)
-    if kv_dtype == GQA_KV_FP8_E4M3:
-        if k_scale is None or v_scale is None:
-            raise ValueError("fp8 KV needs k_scale and v_scale")
-        _need(k_scale, "k_scale", torch.float32, (num_pages, Hk))
-        _need(v_scale, "v_scale", torch.float32, (num_pages, Hk))
+    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
     return B, Hk, D, P, num_pages, kv_dtype
 
 
@@ -316,7 +342,7 @@ def gqa_paged_append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch
                         v_scale: Optional[torch.Tensor] = None,
                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Write token seq_lens[b] - 1 of every sequence (k_new / v_new bf16 [B][Hk][D]) into
-    the paged cache, in place (e4m3 pools quantise it; see include/gqa_paged.h).  Returns
+    the paged cache, in place (e4m3 and 4-bit pools quantise it; see include/gqa_paged.h).  Returns
     the workspace holding the error word."""
     B, Hk, D, P, num_pages, kv_dtype = _append_args(k_new, v_new, k_pages, v_pages, page_table,
                                                      seq_lens, k_scale, v_scale)
@@ -422,6 +448,113 @@ def lse_combine(o_part: torch.Tensor, lse_part: torch.Tensor,
                             _stream(stream))
     _check("lse_combine", st)
     return out, lse
+
+
+def new_fp4_pool(num_pages: int, Hk: int, page_size: int, head_dim: int, device) -> torch.Tensor:
+    """A zero-filled 4-bit pool of keys or of values: uint8 [num_pages][Hk][P][9 * D / 16]."""
+    if head_dim not in (64, 128):
+        raise ValueError("4-bit pools hold head_dim 64 or 128")
+    return torch.zeros(num_pages, Hk, page_size, 9 * head_dim // 16, dtype=torch.uint8,
+                       device=device)
+
+
+def _need_rows(t: torch.Tensor, name: str, shape):
+    """bf16 rows [T][Hk][D]: contiguous inside a row, any distance between rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    T, Hk, D = shape
+    if t.numel() and (t.stride(2) != 1 or (Hk > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name}: the [Hk][head_dim] values of a row must be contiguous")
+    return t.stride(0) if T > 1 else Hk * D
+
+
+def gqa_paged_write_kv(k_new: torch.Tensor, v_new: torch.Tensor, cu_q: torch.Tensor,
+                       k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                       seq_lens: torch.Tensor, max_q_len: int,
+                       k_scale: Optional[torch.Tensor] = None,
+                       v_scale: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Write the newest cu_q[b+1] - cu_q[b] tokens of every sequence (k_new / v_new bf16
+    [total_q][Hk][D], rows of any stride; cu_q int32 [B+1]) into the paged cache, in place;
+    e4m3 and 4-bit pools quantise them (see include/gqa_paged.h).  Returns the workspace holding
+    the error word."""
+    _need(k_pages, "k_pages", _KV_DTYPES)
+    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
+    kv_dtype, D = _kv_layout(k_pages)
+    num_pages, Hk, P, _ = k_pages.shape
+    _need(seq_lens, "seq_lens", torch.int32)
+    B, T = seq_lens.shape[0], k_new.shape[0]
+    ks = _need_rows(k_new, "k_new", (T, Hk, D))
+    vs = _need_rows(v_new, "v_new", (T, Hk, D))
+    _need(cu_q, "cu_q", torch.int32, (B + 1,))
+    _need(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B][pt_stride]")
+    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
+    if workspace is None:
+        workspace = new_workspace(256, k_pages.device)
+    _need(workspace, "workspace", torch.uint8)
+    if T == 0:
+        return workspace
+    st = load().gqa_paged_write_kv(
+        _ptr(k_new), _ptr(v_new), ks, vs, _ptr(cu_q), _ptr(k_pages), _ptr(v_pages),
+        _ptr(k_scale), _ptr(v_scale), kv_dtype, _ptr(page_table), page_table.shape[1],
+        _ptr(seq_lens), B, Hk, D, P, num_pages, T, int(max_q_len), _ptr(workspace),
+        _stream(stream))
+    _check("gqa_paged_write_kv", st)
+    return workspace
+
+
+def gqa_paged_read_kv(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                      seq_lens: torch.Tensor, cu_out: torch.Tensor, total: int,
+                      starts: Optional[torch.Tensor] = None,
+                      k_scale: Optional[torch.Tensor] = None,
+                      v_scale: Optional[torch.Tensor] = None, paged: bool = False,
+                      k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Tokens starts[b] (default 0) .. seq_lens[b] - 1 of every sequence as bf16 values, from
+    bf16, e4m3 or 4-bit pools: (k, v) [total][Hk][D] rows at cu_out (int64 [B+1]), or, with
+    `paged`, bf16 pages [total][Hk][P][D] with cu_out counting pages (page cu_out[b] + i holds
+    the i-th page of the stretch; slots outside it are not written)."""
+    _need(k_pages, "k_pages", _KV_DTYPES)
+    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
+    kv_dtype, D = _kv_layout(k_pages)
+    num_pages, Hk, P, _ = k_pages.shape
+    _need(seq_lens, "seq_lens", torch.int32)
+    B = seq_lens.shape[0]
+    _need(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B][pt_stride]")
+    _need(cu_out, "cu_out", torch.int64, (B + 1,))
+    if starts is not None:
+        _need(starts, "starts", torch.int32, (B,))
+    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
+    total = int(total)
+    shape = (total, Hk, P, D) if paged else (total, Hk, D)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+    _need(k_out, "k_out", torch.bfloat16, shape)
+    _need(v_out, "v_out", torch.bfloat16, shape)
+    if workspace is None:
+        workspace = new_workspace(256, k_pages.device)
+    _need(workspace, "workspace", torch.uint8)
+    if total == 0:
+        return k_out, v_out
+    st = load().gqa_paged_read_kv(
+        _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), kv_dtype, _ptr(page_table),
+        page_table.shape[1], _ptr(starts), _ptr(seq_lens), _ptr(cu_out), B, Hk, D, P, num_pages,
+        total, int(bool(paged)), _ptr(k_out), _ptr(v_out), _ptr(workspace), _stream(stream))
+    _check("gqa_paged_read_kv", st)
+    return k_out, v_out
 
 
 def gqa_paged_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,

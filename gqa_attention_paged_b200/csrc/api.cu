@@ -11,6 +11,7 @@
 
 #include "gqa_internal.h"
 #include "gqa_paged.h"
+#include "quant_kv.h"
 
 using namespace gqa;
 
@@ -73,6 +74,10 @@ int encode_q_map(CUtensorMap *map, const void *q, int total_q, int Hq, int D, in
 
 bool valid_page_size(int P) { return P == 16 || P == 32 || P == 64; }
 
+bool known_kv_dtype(int t) {
+    return t == GQA_KV_BF16 || t == GQA_KV_FP8_E4M3 || t == GQA_KV_FP4;
+}
+
 int sm_count();
 
 // Split counts measured on one B200 (148 SMs) with `bench.py --sweep splits` (its summary is
@@ -126,6 +131,7 @@ int clamp_splits(int s, int max_seq_len, int P) {
 // The schedule a decode call runs: 0 = balanced persistent, else the split schedule with
 // that many splits.
 int decode_schedule(int num_splits, int B, int Hk, int max_seq_len, int P, int kv_dtype) {
+    if (kv_dtype == GQA_KV_FP4) return 0;  // the 4-bit decode has one schedule
     if (num_splits > 0) return num_splits;
     if (B > kStreamMaxBatch) return gqa_pick_splits(B, Hk, max_seq_len, P, kv_dtype);
     if (num_splits == GQA_SPLITS_BALANCED || B <= 0 || Hk <= 0 || P <= 0) return 0;
@@ -175,7 +181,7 @@ int decode_check_args(const void *q, const void *k_pages, const void *v_pages,
                       int Hq, int Hk, int head_dim, int page_size, int num_pages, int num_splits,
                       const void *out, const float *lse) {
     if (!q || !k_pages || !v_pages || !page_table || !seq_lens || !out) return GQA_ERR_NULL;
-    if (kv_dtype != GQA_KV_BF16 && kv_dtype != GQA_KV_FP8_E4M3) return GQA_ERR_DTYPE;
+    if (!known_kv_dtype(kv_dtype)) return GQA_ERR_DTYPE;
     if (kv_dtype == GQA_KV_FP8_E4M3 && (!k_scale || !v_scale || head_dim != 128))
         return GQA_ERR_DTYPE;
     if (B < 0 || B > 65535 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0 || Hk > 65535 ||
@@ -183,9 +189,12 @@ int decode_check_args(const void *q, const void *k_pages, const void *v_pages,
         pt_stride <= 0 || (int64_t)num_pages * Hk * page_size > INT32_MAX ||
         (int64_t)pt_stride * page_size > INT32_MAX)
         return GQA_ERR_SHAPE;
-    if (num_splits < GQA_SPLITS_BALANCED || num_splits > GQA_MAX_SPLITS) return GQA_ERR_SPLITS;
+    if (num_splits < GQA_SPLITS_BALANCED || num_splits > GQA_MAX_SPLITS ||
+        (kv_dtype == GQA_KV_FP4 && num_splits > 0))
+        return GQA_ERR_SPLITS;
     if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
-        !aligned(page_table, 4) || !aligned(seq_lens, 4) || (lse && !aligned(lse, 4)))
+        !aligned(page_table, 4) || !aligned(seq_lens, 4) || (lse && !aligned(lse, 4)) ||
+        (kv_dtype == GQA_KV_FP4 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))))
         return GQA_ERR_ALIGN;
     return GQA_OK;
 }
@@ -209,6 +218,35 @@ int decode_call(const void *q, const void *k_pages, const void *v_pages, const f
                                                         num_splits);
     if (!aligned(workspace, 256) || workspace_bytes < need) return GQA_ERR_WORKSPACE;
     if (B == 0) return GQA_OK;
+
+    if (kv_dtype == GQA_KV_FP4) {
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        Fp4DecodeArgs f;
+        f.q = q;
+        f.k_pages = static_cast<const uint8_t *>(k_pages);
+        f.v_pages = static_cast<const uint8_t *>(v_pages);
+        f.k_scale = k_scale;
+        f.v_scale = v_scale;
+        f.page_table = page_table;
+        f.pt_stride = pt_stride;
+        f.seq_lens = seq_lens;
+        f.B = B;
+        f.Hq = Hq;
+        f.Hk = Hk;
+        f.D = head_dim;
+        f.P = page_size;
+        f.num_pages = num_pages;
+        f.scale = scale;
+        f.pack_gqa = pack_gqa ? 1 : 0;
+        f.out = out;
+        f.out_f32 = out_f32;
+        f.lse = lse;
+        f.err = reinterpret_cast<int *>(ws);
+        f.counters = reinterpret_cast<int *>(ws + kWorkspaceHeader);
+        f.pieces = reinterpret_cast<float *>(ws + decode_zero_prefix_bytes(B, Hq));
+        f.sms = sm_count() > kStreamMaxSms ? kStreamMaxSms : sm_count();
+        return launch_decode_fp4(f, stream) == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
+    }
 
     const int64_t rows = (int64_t)num_pages * Hk * page_size;
     CUtensorMap kmap, vmap;
@@ -277,7 +315,7 @@ const char *gqa_status_string(int s) {
 }
 
 int gqa_pick_splits(int B, int Hk, int max_seq_len, int page_size, int kv_dtype) {
-    if (B <= 0 || Hk <= 0 || page_size <= 0 || max_seq_len <= 0) return 1;
+    if (B <= 0 || Hk <= 0 || page_size <= 0 || max_seq_len <= 0 || kv_dtype == GQA_KV_FP4) return 1;
     int ui, ci;
     split_cell(B, Hk, max_seq_len, ui, ci);
     return clamp_splits(kBestSplits[kv_dtype == GQA_KV_FP8_E4M3 ? 1 : 0][ui][ci], max_seq_len,
@@ -286,6 +324,10 @@ int gqa_pick_splits(int B, int Hk, int max_seq_len, int page_size, int kv_dtype)
 
 size_t gqa_paged_decode_workspace_size(int B, int Hq, int Hk, int head_dim, int page_size,
                                        int max_seq_len, int kv_dtype, int num_splits) {
+    if (kv_dtype == GQA_KV_FP4)
+        return B < 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0
+                   ? kWorkspaceHeader
+                   : decode_zero_prefix_bytes(B, Hq) + fp4_decode_piece_bytes(Hq, Hk, head_dim);
     const int S = decode_schedule(num_splits, B, Hk, max_seq_len, page_size, kv_dtype);
     if (S == 0 && Hq > 0 && Hk > 0 && Hq % Hk == 0)
         return decode_zero_prefix_bytes(B, Hq) + stream_k_piece_bytes(Hq, Hk, head_dim);
@@ -303,6 +345,7 @@ int gqa_paged_decode_kernel_launches(int B, int Hq, int Hk, int head_dim, int pa
                                      int pack_gqa) {
     (void)head_dim;
     if (B <= 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0 || page_size <= 0) return 0;
+    if (kv_dtype == GQA_KV_FP4) return num_splits > 0 ? 0 : 1;
     const int S = decode_schedule(num_splits, B, Hk, max_seq_len, page_size, kv_dtype);
     if (S == 0) return decode_defers_merge(B, Hq, Hk, pack_gqa ? 1 : 0, decode_grid()) ? 2 : 1;
     return S > 1 ? 2 : 1;
@@ -435,7 +478,7 @@ int gqa_paged_append_kv(const void *k_new, const void *v_new, void *k_pages, voi
                         int page_size, int num_pages, void *workspace, cudaStream_t stream) {
     if (!k_new || !v_new || !k_pages || !v_pages || !page_table || !seq_lens || !workspace)
         return GQA_ERR_NULL;
-    if (kv_dtype != GQA_KV_BF16 && kv_dtype != GQA_KV_FP8_E4M3) return GQA_ERR_DTYPE;
+    if (!known_kv_dtype(kv_dtype)) return GQA_ERR_DTYPE;
     if (kv_dtype == GQA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return GQA_ERR_DTYPE;
     if (B < 0 || B > 65535 || Hk <= 0 || Hk > 65535 || (head_dim != 64 && head_dim != 128) ||
         !valid_page_size(page_size) || num_pages <= 0 || pt_stride <= 0 ||
@@ -447,6 +490,12 @@ int gqa_paged_append_kv(const void *k_new, const void *v_new, void *k_pages, voi
         !aligned(workspace, 256) || (k_scale && !aligned(k_scale, 4)) ||
         (v_scale && !aligned(v_scale, 4)))
         return GQA_ERR_ALIGN;
+    if (kv_dtype == GQA_KV_FP4) {
+        const long long row = (long long)Hk * head_dim;
+        return gqa_paged_write_kv(k_new, v_new, row, row, nullptr, k_pages, v_pages, k_scale, v_scale,
+                                  kv_dtype, page_table, pt_stride, seq_lens, B, Hk, head_dim, page_size,
+                                  num_pages, B, 1, workspace, stream);
+    }
     AppendArgs a;
     a.k_new = k_new;
     a.v_new = v_new;
@@ -467,6 +516,100 @@ int gqa_paged_append_kv(const void *k_new, const void *v_new, void *k_pages, voi
     return launch_append(a, stream) == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
 }
 
+int gqa_paged_write_kv(const void *k_new, const void *v_new, int64_t k_stride, int64_t v_stride,
+                       const int32_t *cu_q, void *k_pages, void *v_pages, float *k_scale,
+                       float *v_scale, int kv_dtype, const int32_t *page_table, int pt_stride,
+                       const int32_t *seq_lens, int B, int Hk, int head_dim, int page_size,
+                       int num_pages, int total_q, int max_q_len, void *workspace,
+                       cudaStream_t stream) {
+    if (!k_new || !v_new || !k_pages || !v_pages || !page_table || !seq_lens || !workspace)
+        return GQA_ERR_NULL;
+    if (!known_kv_dtype(kv_dtype)) return GQA_ERR_DTYPE;
+    if (kv_dtype == GQA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return GQA_ERR_DTYPE;
+    if (B < 0 || B > 65535 || Hk <= 0 || Hk > 65535 || (head_dim != 64 && head_dim != 128) ||
+        !valid_page_size(page_size) || num_pages <= 0 || pt_stride <= 0 || total_q < 0 ||
+        max_q_len < 0 || (!cu_q && (total_q != B || max_q_len > 1)) ||
+        (int64_t)num_pages * Hk * page_size > INT32_MAX ||
+        (int64_t)pt_stride * page_size > INT32_MAX || k_stride < (int64_t)Hk * head_dim ||
+        v_stride < (int64_t)Hk * head_dim ||
+        ((int64_t)total_q * Hk * (head_dim / 16) + 255) / 256 > INT32_MAX)
+        return GQA_ERR_SHAPE;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
+        !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(page_table, 4) ||
+        !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(workspace, 256) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return GQA_ERR_ALIGN;
+    WriteArgs a;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.cu_q = cu_q;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.kv_dtype = kv_dtype;
+    a.page_table = page_table;
+    a.pt_stride = pt_stride;
+    a.seq_lens = seq_lens;
+    a.B = B;
+    a.Hk = Hk;
+    a.D = head_dim;
+    a.P = page_size;
+    a.num_pages = num_pages;
+    a.total_q = total_q;
+    a.max_q_len = max_q_len;
+    a.err = reinterpret_cast<int *>(workspace);
+    return launch_write_kv(a, stream) == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
+}
+
+int gqa_paged_read_kv(const void *k_pages, const void *v_pages, const float *k_scale,
+                      const float *v_scale, int kv_dtype, const int32_t *page_table, int pt_stride,
+                      const int32_t *starts, const int32_t *seq_lens, const int64_t *cu_out, int B,
+                      int Hk, int head_dim, int page_size, int num_pages, int64_t total, int paged,
+                      void *k_out, void *v_out, void *workspace, cudaStream_t stream) {
+    if (!k_pages || !v_pages || !page_table || !seq_lens || !cu_out || !k_out || !v_out ||
+        !workspace)
+        return GQA_ERR_NULL;
+    if (!known_kv_dtype(kv_dtype)) return GQA_ERR_DTYPE;
+    if (kv_dtype == GQA_KV_FP8_E4M3 && (!k_scale || !v_scale)) return GQA_ERR_DTYPE;
+    if (B < 0 || B > 65535 || Hk <= 0 || Hk > 65535 || (head_dim != 64 && head_dim != 128) ||
+        !valid_page_size(page_size) || num_pages <= 0 || pt_stride <= 0 || total < 0 ||
+        total > INT32_MAX || (int64_t)num_pages * Hk * page_size > INT32_MAX ||
+        (int64_t)pt_stride * page_size > INT32_MAX ||
+        // a thread per (row, kv head, 16 dims) in blocks of 256
+        total * (paged ? page_size : 1) > ((int64_t)INT32_MAX * 256) / ((int64_t)Hk * (head_dim / 16)))
+        return GQA_ERR_SHAPE;
+    if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_out, 16) ||
+        !aligned(v_out, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
+        !aligned(starts, 4) || !aligned(cu_out, 8) || !aligned(workspace, 256) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return GQA_ERR_ALIGN;
+    ReadArgs a;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.page_table = page_table;
+    a.pt_stride = pt_stride;
+    a.starts = starts;
+    a.seq_lens = seq_lens;
+    a.cu_out = cu_out;
+    a.B = B;
+    a.Hk = Hk;
+    a.D = head_dim;
+    a.P = page_size;
+    a.num_pages = num_pages;
+    a.kv_dtype = kv_dtype;
+    a.total = total;
+    a.paged = paged ? 1 : 0;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.err = reinterpret_cast<int *>(workspace);
+    return launch_read_kv(a, stream) == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
+}
+
 int gqa_paged_append_decode(const void *q, const void *k_new, const void *v_new, void *k_pages,
                             void *v_pages, float *k_scale, float *v_scale, int kv_dtype,
                             const int32_t *page_table, int pt_stride, const int32_t *seq_lens,
@@ -476,7 +619,9 @@ int gqa_paged_append_decode(const void *q, const void *k_new, const void *v_new,
     // the decode's checks first, so that a call it would reject changes nothing
     if (!q || !out) return GQA_ERR_NULL;
     if (Hq <= 0 || Hk <= 0 || Hq % Hk != 0) return GQA_ERR_SHAPE;
-    if (num_splits < GQA_SPLITS_BALANCED || num_splits > GQA_MAX_SPLITS) return GQA_ERR_SPLITS;
+    if (num_splits < GQA_SPLITS_BALANCED || num_splits > GQA_MAX_SPLITS ||
+        (kv_dtype == GQA_KV_FP4 && num_splits > 0))
+        return GQA_ERR_SPLITS;
     if (kv_dtype == GQA_KV_FP8_E4M3 && head_dim != 128) return GQA_ERR_DTYPE;
     if (!workspace || !aligned(workspace, 256)) return workspace ? GQA_ERR_WORKSPACE : GQA_ERR_NULL;
     if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||

@@ -37,7 +37,8 @@
  *   - Layouts are row-major (C order).  KV pools are [num_pages][Hk][page_size][head_dim]
  *     ("HND": each (page, kv head) block is one contiguous run).  q and out are bf16.
  *   - Sequence lengths count the current token(s): the new K/V are in the cache, written
- *     by the caller or by gqa_paged_append_kv().  No other call writes the cache.
+ *     by the caller, gqa_paged_append_kv() or gqa_paged_write_kv().  No other call writes
+ *     the cache.
  *   - Page-table entries at or beyond ceil(seq_len / page_size) are never read; entries
  *     may repeat across and within sequences (shared prefix pages).
  *   - A sequence of length 0 yields output 0 and lse = -inf.
@@ -69,8 +70,30 @@ typedef enum {
 
 typedef enum {
     GQA_KV_BF16 = 0,     /* k_pages / v_pages hold bf16 */
-    GQA_KV_FP8_E4M3 = 1  /* k_pages / v_pages hold OCP e4m3 bytes; value = code * scale[page][kv head] */
+    GQA_KV_FP8_E4M3 = 1, /* k_pages / v_pages hold OCP e4m3 bytes; value = code * scale[page][kv head] */
+    GQA_KV_FP4 = 2       /* k_pages / v_pages hold 4-bit tiles: e2m1 codes with an e4m3 scale per
+                            (token, kv head, 16 dims); value = code * scale * k_scale[kv head] */
 } gqa_kv_dtype_t;
+
+/*
+ * 4-bit pools (GQA_KV_FP4): uint8 [num_pages][Hk][page_size][9 * head_dim / 16], 4.5 bits per
+ * element; head_dim 64 or 128.  Written by gqa_paged_write_kv() / gqa_paged_append_kv(), read
+ * by the decode calls and gqa_paged_read_kv().  k_scale / v_scale are one positive fp32 factor
+ * per kv head, [Hk], never written; NULL means 1.
+ *   Values: an e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is the sign) times the block's e4m3
+ *   scale times the head's factor.  A block of 16 dims of one token with largest magnitude a
+ *   is stored, g being the factor and fl() fp32 rounding, as
+ *     scale = e4m3(min(fl(a / fl(6 g)), 448)),  s = fl(scale * g),  code = e2m1(fl(x / s)),
+ *   both conversions to the nearest value, ties to the even code, saturating.  A block whose
+ *   s is 0 stores zeros.  Infinities saturate.  A block that holds a NaN reads back as NaN.
+ *   Layout: each 16 tokens of a (page, kv head) block are one tile of 9 * head_dim bytes,
+ *   8 * head_dim bytes of codes and then head_dim bytes of scales:
+ *     K  codes [16 tokens][head_dim / 2], a byte holding dims 2i (low nibble) and 2i + 1;
+ *        scales [16 tokens][head_dim / 16].
+ *     V  a byte holds one dim of tokens 2i (low nibble) and 2i + 1; with C = head_dim / 8, pair i
+ *        and dim d are byte (i / 4) * 4 * head_dim + (d / C) * 4 * C + (i % 4) * C + d % C;
+ *        scales [8 pairs][head_dim / 16][2 tokens].
+ */
 
 #define GQA_MAX_SPLITS 64
 /* num_splits value that asks for the balanced persistent schedule whatever the problem
@@ -81,6 +104,7 @@ typedef enum {
  * Bytes of workspace gqa_paged_decode() needs for the same B, heads, head_dim, page_size,
  * longest context (pt_stride * page_size), kv_dtype and num_splits.  Layout: a 256-byte
  * header holding the device error word, then
+ *   GQA_KV_FP4: int32 merge counters [B*Hq] (rounded up to 256 bytes) and the merge pieces;
  *   num_splits = 0, B <= 2048 (balanced schedule): int32 merge counters [B*Hq] (rounded
  *     up to 256 bytes) and the merge pieces, 2 per worker of the largest grid
  *     (160 SMs x 2 CTAs x 4 workers), each min(Hq/Hk, 16) x (head_dim + 1) fp32;
@@ -120,7 +144,8 @@ int gqa_pick_splits(int B, int Hk, int max_seq_len, int page_size, int kv_dtype)
  *   k_pages,
  *   v_pages    [num_pages][Hk][page_size][head_dim] of kv_dtype; 16-byte aligned
  *   k_scale,
- *   v_scale    fp32 [num_pages][Hk] for GQA_KV_FP8_E4M3; ignored (may be NULL) for bf16
+ *   v_scale    fp32 [num_pages][Hk] for GQA_KV_FP8_E4M3; [Hk] or NULL for GQA_KV_FP4;
+ *              ignored (may be NULL) for bf16
  *   page_table int32 [B][pt_stride]; pt_stride >= ceil(max seq_len / page_size)
  *   seq_lens   int32 [B], each in [0, pt_stride * page_size]
  *   Hq % Hk == 0; head_dim in {64, 128}; page_size in {16, 32, 64}
@@ -137,6 +162,8 @@ int gqa_pick_splits(int B, int Hk, int max_seq_len, int page_size, int kv_dtype)
  *              1..GQA_MAX_SPLITS: contiguous page-aligned ranges of ceil(np / num_splits)
  *              pages (np = ceil(seq_len / page_size)), merged with lse_combine on the
  *              same stream
+ *              GQA_KV_FP4: 0 or GQA_SPLITS_BALANCED, which are the same schedule (any B);
+ *              GQA_ERR_SPLITS for explicit counts
  *   pack_gqa   1 (default): all heads of a group in one thread block, each KV page read
  *              once; 0: one query head per thread block (for comparison sweeps only)
  *   out        bf16 [B][Hq][head_dim]
@@ -292,11 +319,13 @@ int lse_combine(const float *o_part, const float *lse_part, int num_splits, int 
  *                (fp32; 1 for an all-zero token), a later token keeps the page's scale;
  *                each element is stored as e4m3(x / scale), the fp32 quotient rounded to
  *                nearest even and saturated at +-448.  The same for v.
+ *   4-bit pools: as gqa_paged_write_kv() (k_new and v_new 16-byte aligned).
  * Sequences with seq_lens[b] = 0 append nothing.
  *
  *   k_new, v_new  bf16 [B][Hk][head_dim]
  *   k_pages, v_pages, page_table, seq_lens, page sizes: as for gqa_paged_decode()
- *   k_scale, v_scale  fp32 [num_pages][Hk], read and written for GQA_KV_FP8_E4M3
+ *   k_scale, v_scale  fp32 [num_pages][Hk], read and written for GQA_KV_FP8_E4M3; [Hk]
+ *               or NULL, read, for GQA_KV_FP4
  *   workspace   >= 256 bytes, 256-byte aligned; its error word records a page-table
  *               entry or seq_len out of range (that token is not written)
  * Two sequences whose new tokens fall on the same (page, slot) race.
@@ -321,10 +350,64 @@ int gqa_paged_append_decode(const void *q, const void *k_new, const void *v_new,
                             void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * KV write: the newest Lq_b = cu_q[b+1] - cu_q[b] tokens of every sequence into the paged cache,
+ * quantised for e4m3 and 4-bit pools: a prefill chunk's K and V, written before
+ * gqa_paged_prefill() or kept for later decode steps.  seq_lens[b] already counts them: row
+ * cu_q[b] + i goes to token seq_lens[b] - Lq_b + i.
+ *   bf16 pools:  the rows' bits.
+ *   e4m3 pools:  a page whose first slot is among the chunk's tokens takes, per kv head, the
+ *                scale absmax / 448 (fp32; 1 if all zero) over the chunk's tokens in it; a page
+ *                begun earlier keeps its scale.  Elements as in gqa_paged_append_kv(), which
+ *                is this call for chunks of one token.
+ *   4-bit pools: per block of 16 dims of a token, as described at the top of this file; what a
+ *                token is stored as does not depend on the other tokens.  Nothing but the
+ *                chunk's own nibbles and scales changes.
+ *
+ *   k_new, v_new  bf16 rows [Hk][head_dim], k_stride / v_stride elements apart (at least
+ *               Hk * head_dim, a multiple of 8; e.g. slices of a fused projection); 16-byte
+ *               aligned
+ *   cu_q        int32 [B+1], as for gqa_paged_prefill(); or NULL: one row per sequence
+ *               (total_q = B, max_q_len <= 1), ignored where seq_lens[b] = 0
+ *   total_q     rows of k_new / v_new; max_q_len >= every Lq_b
+ *   the rest as for gqa_paged_append_kv(); pools 16-byte aligned
+ * A sequence whose lengths do not fit (Lq_b above max_q_len or seq_lens[b], seq_lens[b] above
+ * the page table, rows outside total_q) is recorded in the error word and not written, nor
+ * are tokens whose page-table entry is out of range.  Sequences that write the same page race.
+ */
+int gqa_paged_write_kv(const void *k_new, const void *v_new, int64_t k_stride, int64_t v_stride,
+                       const int32_t *cu_q, void *k_pages, void *v_pages, float *k_scale,
+                       float *v_scale, int kv_dtype, const int32_t *page_table, int pt_stride,
+                       const int32_t *seq_lens, int B, int Hk, int head_dim, int page_size,
+                       int num_pages, int total_q, int max_q_len, void *workspace,
+                       cudaStream_t stream);
+
+/*
+ * KV read: tokens starts[b] .. seq_lens[b] - 1 of every sequence as bf16 values, from bf16,
+ * e4m3 or 4-bit pools (code * scale in fp32, exact for 4-bit codes, then times the factor,
+ * then rounded to bf16).
+ *   paged = 0: token t goes to row cu_out[b] + t - starts[b] of k_out / v_out
+ *              [total][Hk][head_dim]; cu_out[b+1] - cu_out[b] = seq_lens[b] - starts[b].
+ *   paged = 1: to page cu_out[b] + t / page_size - starts[b] / page_size, slot t % page_size of
+ *              k_out / v_out [total][Hk][page_size][head_dim], the pools' own layout, e.g. the
+ *              prior context of a gqa_paged_prefill() on bf16 pages; cu_out counts pages.
+ *              Slots outside the stretch are left as they were.
+ *   starts     int32 [B] or NULL (0);  cu_out int64 [B+1], cu_out[0] = 0, nondecreasing
+ *   total      rows (pages) of the outputs; k_out, v_out 16-byte aligned
+ *   k_scale, v_scale, kv_dtype, pools, page_table: as for gqa_paged_write_kv()
+ *   workspace  >= 256 bytes, 256-byte aligned; its error word records page-table entries or
+ *              lengths out of range and rows past the end of their sequence (left unwritten)
+ */
+int gqa_paged_read_kv(const void *k_pages, const void *v_pages, const float *k_scale,
+                      const float *v_scale, int kv_dtype, const int32_t *page_table, int pt_stride,
+                      const int32_t *starts, const int32_t *seq_lens, const int64_t *cu_out, int B,
+                      int Hk, int head_dim, int page_size, int num_pages, int64_t total, int paged,
+                      void *k_out, void *v_out, void *workspace, cudaStream_t stream);
+
+/*
  * Copy-out of the paged cache into contiguous per-sequence storage, bit for bit:
  *   k_out[cu_kv[b] + t][j][:] = k_pages[page_table[b][t / page_size]][j][t % page_size][:]
  * and the same for v, for t < seq_lens[b].  elem_bytes is 2 (bf16) or 1 (fp8); bytes
- * are copied, never interpreted.  A check of the page-table indirection on its own.
+ * are copied, never interpreted (4-bit tiles have no such rows: gqa_paged_read_kv()).  A check of the page-table indirection on its own.
  *
  *   cu_kv    int64 [B+1] output row offsets (cu_kv[b+1] - cu_kv[b] = seq_lens[b])
  *   k_out, v_out  [cu_kv[B]][Hk][head_dim] elements
