@@ -4,7 +4,9 @@ for byte), what the read gives back, the decode over it, and a run of all of the
 Tolerances.  Stored codes and scales are equal.  Values read back: the fp32 product by the factor
 (half a step, 2^-24) and the rounding to bf16 (2^-8), none of which the model's own bf16 rounding may
 cross by more than one step: |err| <= 2^-7 |ref|; without a factor they are equal for 4 bits.  Decode:
-bf16 output (2^-8 |ref|); f16 weights (2^-11 of every term, so 2^-11 sum p |v|); fp32 sums of at
+bf16 output (2^-8 |ref|); f16 weights (2^-11 of every term, so 2^-11 sum p |v|; where a weight is subnormal
+half of f16's smallest step, 2^-25, on the scale on which the largest weight is 2^7 at least: 2^-32 sum |v|
+beside a largest normalised weight of at most 1); fp32 sums of at
 most a few thousand terms and the exponential (2^-17 sum p |v|); a score error e changes every weight by a
 relative 2 e at most, with e <= 2^-17 scale sum |q| |k| (D products added in fp32, in any order, and the
 scale).  lse: e + 2^-20 (log and exp)."""
@@ -309,14 +311,16 @@ def test_read_records_rows_past_the_sequence():
 def expect(c, q, scale):
     B = q.shape[0]
     res = [M.attention(q[b].double().numpy(), c.values(b, 0), c.values(b, 1), scale) for b in range(B)]
-    return [np.stack([x[i] for x in res]) for i in range(4)]
+    sv = [np.repeat(np.abs(c.values(b, 1)).sum(0), q.shape[1] // c.Hk, 0) for b in range(B)]
+    return [np.stack([x[i] for x in res]) for i in range(4)] + [np.stack(sv)]
 
 
 def close(out, lse, ref, f32_out=False):
-    o, l, pv, big = ref
+    o, l, pv, big, sv = ref
     got = out.double().cpu().numpy()
     e = 2.0 ** -17 * big
-    tol = (0 if f32_out else 2.0 ** -8) * np.abs(o) + (2.0 ** -11 + 2.0 ** -17 + 2 * e[..., None]) * pv + 1e-30
+    tol = (0 if f32_out else 2.0 ** -8) * np.abs(o) + (2.0 ** -11 + 2.0 ** -17 + 2 * e[..., None]) * pv \
+        + 2.0 ** -32 * sv + 1e-30
     bad = ~(np.abs(got - o) <= tol)
     assert not bad.any(), f"{int(bad.sum())} of {bad.size}: worst {np.nanmax(np.abs(got - o) / tol):.2f} times the tolerance"
     if lse is not None:
@@ -324,7 +328,7 @@ def close(out, lse, ref, f32_out=False):
         fin = np.isfinite(l)
         assert np.array_equal(fin, np.isfinite(g))
         assert np.all(g[~fin] == -np.inf)
-        assert np.all(np.abs(g - l)[fin] <= (e + 2.0 ** -20 + 2.0 ** -23 * np.abs(l))[fin])
+        assert np.all(np.abs(g[fin] - l[fin]) <= (e + 2.0 ** -20 + 2.0 ** -23 * np.abs(l))[fin])
 
 
 def queries(c, B, Hq, seed=1):
