@@ -78,6 +78,12 @@ bool known_kv_dtype(int t) {
     return t == GQA_KV_BF16 || t == GQA_KV_FP8_E4M3 || t == GQA_KV_FP4;
 }
 
+// The 4-bit decode counts the batch's steps of 32 tokens in an int.
+bool fp4_steps_fit(int B, int Hq, int pt_stride, int P) {
+    const int64_t rows = (int64_t)B * Hq;
+    return rows <= INT32_MAX && rows * (((int64_t)pt_stride * P + 31) / 32) <= INT32_MAX;
+}
+
 int sm_count();
 
 // Split counts measured on one B200 (148 SMs) with `bench.py --sweep splits` (its summary is
@@ -187,7 +193,8 @@ int decode_check_args(const void *q, const void *k_pages, const void *v_pages,
     if (B < 0 || B > 65535 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0 || Hk > 65535 ||
         (head_dim != 64 && head_dim != 128) || !valid_page_size(page_size) || num_pages <= 0 ||
         pt_stride <= 0 || (int64_t)num_pages * Hk * page_size > INT32_MAX ||
-        (int64_t)pt_stride * page_size > INT32_MAX)
+        (int64_t)pt_stride * page_size > INT32_MAX ||
+        (kv_dtype == GQA_KV_FP4 && !fp4_steps_fit(B, Hq, pt_stride, page_size)))
         return GQA_ERR_SHAPE;
     if (num_splits < GQA_SPLITS_BALANCED || num_splits > GQA_MAX_SPLITS ||
         (kv_dtype == GQA_KV_FP4 && num_splits > 0))
@@ -619,6 +626,9 @@ int gqa_paged_append_decode(const void *q, const void *k_new, const void *v_new,
     // the decode's checks first, so that a call it would reject changes nothing
     if (!q || !out) return GQA_ERR_NULL;
     if (Hq <= 0 || Hk <= 0 || Hq % Hk != 0) return GQA_ERR_SHAPE;
+    if (kv_dtype == GQA_KV_FP4 && B > 0 && pt_stride > 0 && page_size > 0 &&
+        !fp4_steps_fit(B, Hq, pt_stride, page_size))
+        return GQA_ERR_SHAPE;
     if (num_splits < GQA_SPLITS_BALANCED || num_splits > GQA_MAX_SPLITS ||
         (kv_dtype == GQA_KV_FP4 && num_splits > 0))
         return GQA_ERR_SPLITS;

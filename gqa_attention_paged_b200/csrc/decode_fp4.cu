@@ -5,11 +5,11 @@
 // 效优化实践", section "核心参数调优：PackGQA与NumSplits的协同舞蹈"), so every cached byte crosses HBM
 // once; the softmax is the online form ("TensorRT-LLM与TensorRT核心差异解析", section 4.2.1).
 //
-// Schedule.  The 16-token tiles of all (sequence, kv head [, block of heads]) units are laid end
+// Schedule.  The 32-token steps of all (sequence, kv head [, block of heads]) units are laid end
 // to end and cut into equal contiguous shares, one per warp of a fixed grid.  A warp streams its
-// share through a private shared-memory ring: the lane that holds a tile's page index issues its
-// two bulk copies (a tile's codes and scales are contiguous), the warp waits on the slot's mbarrier,
-// takes the tile into registers and hands the slot to the copy of the tile kStages further on.  No
+// share through a private shared-memory ring: the lane that holds a step's page indices issues its
+// bulk copies (a tile's codes and scales are contiguous), the warp waits on the slot's mbarrier,
+// takes the step into registers and hands the slot to the copy of the step kStages further on.  No
 // warp waits for another until the end.  Units cut between the warps of a CTA are then merged
 // through shared memory; those cut between CTAs leave one piece per CTA in the workspace, and the
 // last CTA to arrive merges them, in the order of the CTAs.
@@ -33,8 +33,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // when a score passes it by kLazyRef: weights stay below 2^15, inside f16, and the largest is at
 // least 2^kRefBelow, so that f16's subnormal step costs a small weight 2^-32 of the largest.
 constexpr float kRefBelow = 7.0f, kLazyRef = 15.0f;
-constexpr int kMinTilesPerWarp = 4;
-constexpr int kRuns = kThreads;   // the sequences' tile prefix is kept per run of ceil(B / kRuns)
+constexpr float kNoRef = -3e38f;  // below every reference
+constexpr int kStep = 2 * kFp4Tile;  // tokens of a step: two tiles
+constexpr int kMinSteps = 2;         // steps per warp below which fewer CTAs work
+constexpr int kRuns = kThreads;      // the sequences' step prefix is kept per run of ceil(B / kRuns)
 
 template <int NT>
 constexpr int ctas_per_sm() { return NT == 1 ? 2 : 1; }
@@ -44,23 +46,29 @@ struct Cfg {
     static constexpr int KS = D / 16;         // k steps of the scores, 16-dim tiles of the output
     static constexpr int C = D / 8;           // dims of a lane's V codes
     static constexpr int kTile = fp4_tile_bytes(D);
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr int HW = 8 * NT;         // packed head columns
     static constexpr int RS = D + 4;          // padded row of a dumped state
     static constexpr int kDump = HW * (RS + 2);  // floats: O rows, then m and l
 };
 
+// The unit that a dumped state belongs to: its first step in the batch's order, its steps.
+struct Cut {
+    int unit, first, steps;
+};
+
 template <int D, int NT>
 struct alignas(128) Smem {
     using C = Cfg<D, NT>;
-    uint8_t ring[kWarps][C::kStages][2][C::kTile];  // at the end: the state of the unit begun last
+    uint8_t ring[kWarps][C::kStages][4][C::kTile];  // K, K, V, V; at the end: the state of the unit begun last
     float head[kWarps][C::kDump];                   // the state of a unit begun by an earlier warp
     uint64_t full[kWarps][C::kStages];
-    long long pre[kRuns + 1];                       // tiles before each run of sequences
-    long long wsum[kWarps];
-    int head_unit[kWarps], tail_unit[kWarps];       // unit indices, -1: none
+    int pre[kRuns + 1];                             // steps before each run of sequences
+    int len[kRuns];                                 // tokens, when a run is one sequence
+    int wsum[kWarps];
+    Cut cut[2][kWarps];                             // of head and ring; unit -1: no state
     int empty[kWarps];
-    int abort_flag, last[2];
+    int abort_flag, last[2], first[2];
     static_assert(sizeof(float) * C::kDump <= sizeof(ring[0]), "a state fits the warp's ring");
 };
 
@@ -79,74 +87,98 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return d;
 }
 
-__device__ __forceinline__ int clamped_len(const Fp4DecodeArgs &a, int b) {
-    const int L = __ldg(a.seq_lens + b), most = a.pt_stride * a.P;
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t (&r)[W], const uint8_t *p) {
+    if constexpr (W == 4) *reinterpret_cast<uint4 *>(r) = *reinterpret_cast<const uint4 *>(p);
+    else *reinterpret_cast<uint2 *>(r) = *reinterpret_cast<const uint2 *>(p);
+}
+
+__device__ __forceinline__ int clamped(const Fp4DecodeArgs &a, int L) {
+    const int most = a.pt_stride * a.P;
     return L < 0 ? 0 : (L > most ? most : L);
 }
-__device__ __forceinline__ int tiles_of(int L) { return (L + kFp4Tile - 1) / kFp4Tile; }
+__device__ __forceinline__ int clamped_len(const Fp4DecodeArgs &a, int b) { return clamped(a, __ldg(a.seq_lens + b)); }
+__device__ __forceinline__ int steps_of(int L) { return (int)(((unsigned)L + kStep - 1) / kStep); }
 
-// A tile's place: sequence, unit within it (kv head * head blocks + block), tile of nt.
-struct Pos {
-    int b, y, tile, nt;
+// The batch as every warp sees it: units of a sequence, sequences of a run, and in shared memory
+// the steps before each run (times U: the flat index of its first step) and the lengths.  The host
+// keeps all step indices within an int.
+struct Batch {
+    const Fp4DecodeArgs &a;
+    const int *pre, *lens;
+    int U, per;
+    __device__ __forceinline__ int len(int b) const { return per == 1 ? lens[b] : clamped_len(a, b); }
+    __device__ __forceinline__ int steps(int b) const { return steps_of(len(b)); }
 };
 
-// Step n tiles on (not past the last tile of the batch).
-__device__ __forceinline__ void advance(Pos &p, int n, const Fp4DecodeArgs &a, int U) {
-    p.tile += n;
-    while (p.tile >= p.nt) {
-        p.tile -= p.nt;
-        if (++p.y < U) continue;
-        p.y = 0;
+// A step's place: sequence, unit within it (kv head * head blocks + block), step of the unit's nt.
+struct Pos {
+    int b, y, step, nt;
+};
+
+// n steps on (not past the last step of the batch).
+__device__ __forceinline__ void advance(Pos &p, int n, const Batch &bt) {
+    p.step += n;
+    if (p.step < p.nt) return;
+    unsigned flat = (unsigned)p.y * p.nt + p.step;
+    while (flat >= (unsigned)bt.U * p.nt) {
+        flat -= (unsigned)bt.U * p.nt;
         do {
-            if (++p.b >= a.B) {
-                p.b = a.B - 1;
-                p.tile = 0;
-                p.nt = 1;
+            if (++p.b >= bt.a.B) {
+                p = {bt.a.B - 1, 0, 0, 1};
                 return;
             }
-            p.nt = tiles_of(clamped_len(a, p.b));
+            p.nt = bt.steps(p.b);
         } while (p.nt == 0);
     }
+    p.y = flat / p.nt;
+    p.step = flat - p.y * p.nt;
 }
 
-// The place of flat tile f (a whole warp calls it with the same f).
-__device__ __forceinline__ Pos locate(long long f, const long long *pre, const Fp4DecodeArgs &a, int U,
-                                      int lane) {
-    int lo = 0, hi = kRuns - 1;  // first run with U * pre[run + 1] > f
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (U * pre[mid + 1] > f) hi = mid;
-        else lo = mid + 1;
-    }
-    const int per = (a.B + kRuns - 1) / kRuns;
-    long long local = f - U * pre[lo];
-    int b = lo * per;
-    Pos p;
-    if (per > 1) {
-        for (const int end = min(a.B, b + per); b < end; b += 32) {
-            const int nt = b + lane < end ? tiles_of(clamped_len(a, b + lane)) : 0;
-            long long incl = nt;
+// The place of step f (a whole warp calls it with the same f).
+__device__ __forceinline__ Pos locate(int f, const Batch &bt, int lane) {
+    // the first run that ends behind f, by its eighth and then its place there
+    static_assert(kRuns == 256, "32 lanes of 8 runs");
+    int run = (__ffs(__ballot_sync(kFull, bt.U * bt.pre[8 * lane + 8] > f)) - 1) * 8;
+    run += __ffs(__ballot_sync(kFull, bt.U * bt.pre[run + (lane & 7) + 1] > f)) - 1;
+    unsigned local = f - bt.U * bt.pre[run];
+    int b = run * bt.per;
+    if (bt.per > 1) {
+        for (const int end = min(bt.a.B, b + bt.per); b < end; b += 32) {
+            const int nt = b + lane < end ? bt.steps(b + lane) : 0;
+            int incl = nt;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(kFull, incl, o);
+                const int t = __shfl_up_sync(kFull, incl, o);
                 if (lane >= o) incl += t;
             }
-            const unsigned past = __ballot_sync(kFull, U * incl > local);
+            const unsigned past = __ballot_sync(kFull, (unsigned)(bt.U * incl) > local);
             if (past) {
                 const int src = __ffs(past) - 1;
-                local -= U * __shfl_sync(kFull, incl - nt, src);
+                local -= bt.U * __shfl_sync(kFull, incl - nt, src);
                 b += src;
                 break;
             }
-            local -= U * __shfl_sync(kFull, incl, 31);
+            local -= bt.U * __shfl_sync(kFull, incl, 31);
         }
     }
+    Pos p;
     p.b = b;
-    p.nt = tiles_of(clamped_len(a, b));
-    p.y = (int)(local / p.nt);
-    p.tile = (int)(local % p.nt);
+    p.nt = bt.steps(b);
+    p.y = local / p.nt;
+    p.step = local - p.y * p.nt;
     return p;
 }
+
+// The batch's steps in equal shares, the first `rem` of them one longer.
+struct Shares {
+    int q, rem;
+    __device__ __forceinline__ int start(int w) const { return w * q + min(w, rem); }
+    __device__ __forceinline__ int owner(int f) const {
+        const int big = rem * (q + 1);
+        return f < big ? f / (q + 1) : rem + (f - big) / q;
+    }
+};
 
 // One warp's attention over part of a unit: lane (gq = lane / 4, cq = lane % 4).
 template <int D, int NT>
@@ -162,8 +194,7 @@ struct State {
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int dt = 0; dt < C::KS; ++dt) o[nt][dt][0] = o[nt][dt][1] = o[nt][dt][2] = o[nt][dt][3] = 0.f;
-            m[nt][0] = m[nt][1] = -INFINITY;
-            l[nt][0] = l[nt][1] = 0.f;
+            m[nt][0] = m[nt][1] = l[nt][0] = l[nt][1] = 0.f;
         }
     }
 
@@ -197,137 +228,140 @@ struct State {
         }
     }
 
-    // Fold in one tile at kt / vt, its first `valid` tokens.  `release` runs once the tile is in
-    // registers.
+    // Fold in a step's two tiles, `valid` tokens of them; `fresh`: the first since reset().  `release`
+    // runs once the step is in registers.
     template <typename F>
-    __device__ __forceinline__ void tile(const uint8_t *kt, const uint8_t *vt, int valid, int lane, F release) {
-        constexpr int KS = C::KS, W = D / 32;  // 32-bit words of a lane's codes per token row / pair
+    __device__ __forceinline__ void step(const uint8_t *slot, int valid, bool fresh, int lane, F release) {
+        constexpr int W = D / 32;  // 32-bit words of a lane's codes per token row / pair
         const int gq = lane >> 2, cq = lane & 3;
-        uint32_t kr[2][W], vr[2][W], ksc[2], vsc[2];
-        const uint8_t *kp = kt + gq * (D / 2) + cq * (D / 8);
-        const uint8_t *vp = vt + gq * (4 * C::C) + cq * C::C;
-        if constexpr (W == 4) {
-            *reinterpret_cast<uint4 *>(kr[0]) = *reinterpret_cast<const uint4 *>(kp);
-            *reinterpret_cast<uint4 *>(kr[1]) = *reinterpret_cast<const uint4 *>(kp + 8 * (D / 2));
-            *reinterpret_cast<uint4 *>(vr[0]) = *reinterpret_cast<const uint4 *>(vp);
-            *reinterpret_cast<uint4 *>(vr[1]) = *reinterpret_cast<const uint4 *>(vp + 4 * D);
-        } else {
-            *reinterpret_cast<uint2 *>(kr[0]) = *reinterpret_cast<const uint2 *>(kp);
-            *reinterpret_cast<uint2 *>(kr[1]) = *reinterpret_cast<const uint2 *>(kp + 8 * (D / 2));
-            *reinterpret_cast<uint2 *>(vr[0]) = *reinterpret_cast<const uint2 *>(vp);
-            *reinterpret_cast<uint2 *>(vr[1]) = *reinterpret_cast<const uint2 *>(vp + 4 * D);
+        const uint8_t *kp = slot + gq * (D / 2) + cq * (D / 8);
+        const uint8_t *ksp = slot + 8 * D + gq * (D / 16) + (D == 128 ? 2 * cq : cq);
+        const uint8_t *vp = slot + 2 * C::kTile + gq * (4 * C::C) + cq * C::C;
+        const uint8_t *vsp = slot + 2 * C::kTile + 8 * D + cq * (D / 8) + (gq * C::C / 16) * 2;
+        uint32_t kr[4][W], ks[4], vr[4][W], vs[4];  // rows (pairs) of tile h: 2 h and 2 h + 1
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const int at = (h >> 1) * C::kTile;
+            load_words(kr[h], kp + at + (h & 1) * (8 * D / 2));
+            if constexpr (D == 128) ks[h] = *reinterpret_cast<const uint16_t *>(ksp + at + (h & 1) * (8 * D / 16));
+            else ks[h] = ksp[at + (h & 1) * (8 * D / 16)] * 0x0101u;
         }
-        // K scales: of the lane's dims, two blocks per row (D = 128) or one
-        const uint8_t *ks0 = kt + 8 * D + gq * (D / 16);
-        if constexpr (D == 128) {
-            ksc[0] = *reinterpret_cast<const uint16_t *>(ks0 + 2 * cq);
-            ksc[1] = *reinterpret_cast<const uint16_t *>(ks0 + 8 * (D / 16) + 2 * cq);
-        } else {
-            ksc[0] = ks0[cq] * 0x0101u;
-            ksc[1] = ks0[8 * (D / 16) + cq] * 0x0101u;
+
+        // ---- scores, a chain per tile
+        float s[2][NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[h][nt][0] = s[h][nt][1] = s[h][nt][2] = s[h][nt][3] = 0.f;
+        uint32_t sc[4][2];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const uint32_t two = e4m3x2_to_f16(ks[h]);
+            sc[h][0] = __byte_perm(two, two, 0x1010);
+            sc[h][1] = __byte_perm(two, two, 0x3232);
         }
-        // V scales: of block (gq C) / 16, tokens 2 cq and + 1, and 8 further
-        const uint8_t *vs0 = vt + 8 * D + cq * (D / 8) + (gq * C::C / 16) * 2;
-        vsc[0] = *reinterpret_cast<const uint16_t *>(vs0);
-        vsc[1] = *reinterpret_cast<const uint16_t *>(vs0 + 4 * (D / 8));
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const int blk = i / 2;  // 16 dims
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t ha[4], hb[4];
+                e2m1x8_to_f16(kr[2 * h][i], ha);
+                e2m1x8_to_f16(kr[2 * h + 1][i], hb);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t af[4] = {hmul2(ha[2 * k], sc[2 * h][blk]), hmul2(hb[2 * k], sc[2 * h + 1][blk]),
+                                            hmul2(ha[2 * k + 1], sc[2 * h][blk]), hmul2(hb[2 * k + 1], sc[2 * h + 1][blk])};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(s[h][nt], af, qf[nt][2 * i + k][0], qf[nt][2 * i + k][1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const int at = (h >> 1) * C::kTile;
+            load_words(vr[h], vp + at + (h & 1) * (4 * D));
+            vs[h] = *reinterpret_cast<const uint16_t *>(vsp + at + (h & 1) * (4 * D / 8));
+        }
         __syncwarp();
         release();
 
-        // ---- scores; even and odd k steps in two chains
-        float s[NT][4], s2[NT][4];
+        // ---- online softmax in log2 units, scores less the reference; only the steps that move the
+        // reference take the column maxima and a rescale
+        float top = -INFINITY;
+        if (valid < kStep) {  // what follows the sequence may be anything: its scores and scales go
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
-        uint32_t ka = e4m3x2_to_f16(ksc[0]), kb = e4m3x2_to_f16(ksc[1]);
-        const uint32_t sa[2] = {__byte_perm(ka, ka, 0x1010), __byte_perm(ka, ka, 0x3232)};
-        const uint32_t sb[2] = {__byte_perm(kb, kb, 0x1010), __byte_perm(kb, kb, 0x3232)};
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            uint32_t ha[4], hb[4];
-            e2m1x8_to_f16(kr[0][i], ha);
-            e2m1x8_to_f16(kr[1][i], hb);
-            const int blk = i / 2;  // 16 dims
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t af[4] = {hmul2(ha[2 * k], sa[blk]), hmul2(hb[2 * k], sb[blk]),
-                                        hmul2(ha[2 * k + 1], sa[blk]), hmul2(hb[2 * k + 1], sb[blk])};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16(k ? s2[nt] : s[nt], af, qf[nt][2 * i + k][0], qf[nt][2 * i + k][1]);
+            for (int h = 0; h < 4; ++h) {
+                if (2 * cq + 8 * h >= valid) vs[h] = 0u;
+                if (2 * cq + 8 * h + 1 >= valid) vs[h] &= 0xffu;
             }
         }
-
-        // ---- online softmax in log2 units; only the tiles that move the reference m take the
-        // column maxima and a rescale
-        float x[NT][4];
-        bool need = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[nt][e] = (s[nt][e] + s2[nt][e]) * kmul[nt][e & 1];
-            if (valid < kFp4Tile) {
-                if (gq >= valid) x[nt][0] = x[nt][1] = -INFINITY;
-                if (gq + 8 >= valid) x[nt][2] = x[nt][3] = -INFINITY;
-            }
-            need |= fmaxf(x[nt][0], x[nt][2]) > m[nt][0] + kLazyRef;
-            need |= fmaxf(x[nt][1], x[nt][3]) > m[nt][1] + kLazyRef;
-        }
-        if (valid < kFp4Tile) {  // what follows the sequence may be anything: its scales become 0
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (2 * cq + 8 * i >= valid) vsc[i] = 0u;
-                if (2 * cq + 8 * i + 1 >= valid) vsc[i] &= 0xffu;
-            }
-        }
-        if (__any_sync(kFull, need)) {
+                for (int e = 0; e < 4; ++e) {
+                    s[h][nt][e] = fmaf(s[h][nt][e], kmul[nt][e & 1], -m[nt][e & 1]);
+                    if (valid < kStep && gq + 8 * (2 * h + (e >> 1)) >= valid) s[h][nt][e] = -INFINITY;
+                    top = fmaxf(top, s[h][nt][e]);
+                }
+        if (__any_sync(kFull, top > kLazyRef || fresh)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float alpha[2];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(x[nt][e], x[nt][e + 2]);
+                    float mx = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
                     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
                     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
                     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                    mx = fmaxf(mx - kRefBelow, m[nt][e]);
-                    alpha[e] = mx == -INFINITY ? 1.f : ex2_approx(m[nt][e] - mx);
-                    m[nt][e] = mx;
-                    l[nt][e] *= alpha[e];
+                    // 0 where the head's reference stays; it may begin anywhere
+                    const float up = fresh ? mx - kRefBelow : fmaxf(mx - kRefBelow, 0.f);
+                    const float alpha = fresh ? 1.f : ex2_approx(-up);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        s[h][nt][e] -= up;
+                        s[h][nt][e + 2] -= up;
+                    }
+                    m[nt][e] += up;
+                    l[nt][e] *= alpha;
+#pragma unroll
+                    for (int dt = 0; dt < C::KS; ++dt) {
+                        o[nt][dt][e] *= alpha;
+                        o[nt][dt][e + 2] *= alpha;
+                    }
                 }
-#pragma unroll
-                for (int dt = 0; dt < KS; ++dt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[nt][dt][e] *= alpha[e & 1];
-            }
         }
-        uint32_t pb[NT][2];
+        uint32_t pb[2][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float p[4];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float ref = m[nt][e & 1] == -INFINITY ? 0.f : m[nt][e & 1];
-                p[e] = ex2_approx(x[nt][e] - ref);
+            for (int nt = 0; nt < NT; ++nt) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) p[e] = ex2_approx(s[h][nt][e]);
+                l[nt][0] += p[0] + p[2];
+                l[nt][1] += p[1] + p[3];
+                pb[h][nt][0] = movmatrix_trans(pack_f16(p[0], p[1]));
+                pb[h][nt][1] = movmatrix_trans(pack_f16(p[2], p[3]));
             }
-            l[nt][0] += p[0] + p[2];
-            l[nt][1] += p[1] + p[3];
-            pb[nt][0] = movmatrix_trans(pack_f16(p[0], p[1]));
-            pb[nt][1] = movmatrix_trans(pack_f16(p[2], p[3]));
-        }
 
         // ---- O^T += V^T P^T
-        const uint32_t va = e4m3x2_to_f16(vsc[0]), vb = e4m3x2_to_f16(vsc[1]);
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            uint32_t ha[4], hb[4];
-            e2m1x8_to_f16(vr[0][i], ha);
-            e2m1x8_to_f16(vr[1][i], hb);
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t va = e4m3x2_to_f16(vs[2 * h]), vb = e4m3x2_to_f16(vs[2 * h + 1]);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t af[4] = {hmul2(ha[2 * k], va), hmul2(ha[2 * k + 1], va), hmul2(hb[2 * k], vb),
-                                        hmul2(hb[2 * k + 1], vb)};
+            for (int i = 0; i < W; ++i) {
+                uint32_t ha[4], hb[4];
+                e2m1x8_to_f16(vr[2 * h][i], ha);
+                e2m1x8_to_f16(vr[2 * h + 1][i], hb);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * i + k], af, pb[nt][0], pb[nt][1]);
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t af[4] = {hmul2(ha[2 * k], va), hmul2(ha[2 * k + 1], va), hmul2(hb[2 * k], vb),
+                                            hmul2(hb[2 * k + 1], vb)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * i + k], af, pb[h][nt][0], pb[h][nt][1]);
+                }
             }
         }
     }
@@ -373,21 +407,37 @@ __device__ __forceinline__ void store4(void *out, int f32, size_t idx, float4 v)
     }
 }
 
-// The output of a finished unit from its merged state: O / l times the values' factor.
-__device__ __forceinline__ float4 normalised(float4 o, float l, float vf) {
-    const float r = l == 0.f ? 0.f : vf / l;
-    return make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+// The V dims at `idx` of a row, times r.
+template <int V>
+__device__ __forceinline__ void store_dims(void *out, int f32, size_t idx, const float (&x)[V], float r) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        if (f32) reinterpret_cast<float2 *>(out)[(idx + i) / 2] = make_float2(x[i] * r, x[i + 1] * r);
+        else reinterpret_cast<uint32_t *>(out)[(idx + i) / 2] = pack_bf16(x[i] * r, x[i + 1] * r);
+    }
 }
 
-__device__ __forceinline__ void add4(float4 &acc, float w, const float4 &o) {
-    acc.x += w * o.x;
-    acc.y += w * o.y;
-    acc.z += w * o.z;
-    acc.w += w * o.w;
-}
+// The query heads of unit y of sequence b: kv head, first row of q, heads.
+struct Heads {
+    int kvh, n;
+    size_t row0;
+    __device__ __forceinline__ Heads(const Fp4DecodeArgs &a, int blocks, int hpc, int b, int y) {
+        const int g = a.Hq / a.Hk;
+        kvh = blocks == 1 ? y : y / blocks;
+        const int h0 = (y - kvh * blocks) * hpc;
+        n = min(hpc, g - h0);
+        row0 = (size_t)b * a.Hq + kvh * g + h0;
+    }
+};
 
-// Weight of a state with reference m in a merge with reference M.
-__device__ __forceinline__ float weight(float m, float M) { return m == -INFINITY ? 0.f : ex2_approx(m - M); }
+// Lane's V dims of a head from its merged state: O / l times the values' factor; lse.
+template <int V>
+__device__ __forceinline__ void put_head(const Fp4DecodeArgs &a, const Heads &hd, int h, int lane, const float (&o)[V],
+                                         float m, float l) {
+    const float vf = a.v_scale ? __ldg(a.v_scale + hd.kvh) : 1.f;
+    store_dims<V>(a.out, a.out_f32, (hd.row0 + h) * (32 * V) + lane * V, o, l == 0.f ? 0.f : vf / l);
+    if (lane == 0 && a.lse) a.lse[hd.row0 + h] = (m + log2f(l)) * kLn2;
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
@@ -397,7 +447,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
     extern __shared__ uint8_t smem_raw[];
     Smem<D, NT> &sm = *reinterpret_cast<Smem<D, NT> *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = a.Hq / a.Hk, U = a.Hk * blocks;
+    const int U = a.Hk * blocks;
+    const Batch bt = {a, sm.pre, sm.len, U, a.B <= kRuns ? 1 : (a.B + kRuns - 1) / kRuns};
 
     if (lane < S) mbar_init(&sm.full[warp][lane], 1);
     if (threadIdx.x == 0) sm.abort_flag = 0;
@@ -408,151 +459,168 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
     grid_dependency_wait();
     grid_dependents_launch();
 
-    // ---- tiles before each run of sequences
+    // ---- steps before each run of sequences
+    int none = 0;  // a sequence without tokens?
     {
-        const int per = (a.B + kRuns - 1) / kRuns;
-        const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
-        long long sum = 0;
+        const int b0 = min(a.B, (int)threadIdx.x * bt.per), b1 = min(a.B, b0 + bt.per);
+        int sum = 0;
         for (int b = b0; b < b1; ++b) {
-            const int L = __ldg(a.seq_lens + b);
-            if (L < 0 || L > a.pt_stride * a.P) {
-                if (blockIdx.x == 0) set_error(a.err, GQA_ERR_BAD_PAGE);
-            }
-            sum += tiles_of(clamped_len(a, b));
+            const int L0 = __ldg(a.seq_lens + b), L = clamped(a, L0);
+            if (L != L0 && blockIdx.x == 0) set_error(a.err, GQA_ERR_BAD_PAGE);
+            if (bt.per == 1) sm.len[b] = L;
+            sum += steps_of(L);
+            none |= L == 0;
         }
-        long long incl = sum;
+        int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(kFull, incl, o);
+            const int t = __shfl_up_sync(kFull, incl, o);
             if (lane >= o) incl += t;
         }
         if (lane == 31) sm.wsum[warp] = incl;
         __syncthreads();
-        for (int w = 0; w < warp; ++w) incl += sm.wsum[w];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) incl += w < warp ? sm.wsum[w] : 0;
         sm.pre[threadIdx.x + 1] = incl;
         if (threadIdx.x == 0) sm.pre[0] = 0;
-        __syncthreads();
+        none = __syncthreads_or(none);
     }
-    const long long T = (long long)U * sm.pre[kRuns];
+    const int T = U * sm.pre[kRuns];
 
-    // sequences without tokens: zeros and -inf
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        if (clamped_len(a, b) != 0) continue;
-        for (int e = threadIdx.x; e < a.Hq * D / 4; e += kThreads)
-            store4(a.out, a.out_f32, (size_t)b * a.Hq * D + 4 * e, make_float4(0.f, 0.f, 0.f, 0.f));
-        if (a.lse)
-            for (int e = threadIdx.x; e < a.Hq; e += kThreads) a.lse[(size_t)b * a.Hq + e] = -INFINITY;
+    if (none) {  // zeros and -inf
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            if (bt.len(b) != 0) continue;
+            for (int e = threadIdx.x; e < a.Hq * D / 4; e += kThreads)
+                store4(a.out, a.out_f32, (size_t)b * a.Hq * D + 4 * e, make_float4(0.f, 0.f, 0.f, 0.f));
+            if (a.lse)
+                for (int e = threadIdx.x; e < a.Hq; e += kThreads) a.lse[(size_t)b * a.Hq + e] = -INFINITY;
+        }
     }
-    const long long NC = max(1LL, min((long long)gridDim.x, T / (kWarps * kMinTilesPerWarp)));  // CTAs with work
+    // CTAs with work
+    const int NC = max(1, min((int)gridDim.x, T / (kWarps * kMinSteps)));
     if (T == 0 || blockIdx.x >= NC) return;
 
-    // ---- this warp's share [s_w, s_w + n)
-    const long long s_w = ((long long)blockIdx.x * kWarps + warp) * T / (NC * kWarps);
-    const long long n = ((long long)blockIdx.x * kWarps + warp + 1) * T / (NC * kWarps) - s_w;
-    int head_unit = -1, tail_unit = -1;
+    // ---- this warp's share: steps [s_w, s_w + n)
+    Shares sh;
+    sh.q = (unsigned)T / (unsigned)(NC * kWarps);
+    sh.rem = T - sh.q * (NC * kWarps);
+    const int s_w = sh.start(blockIdx.x * kWarps + warp);
+    const int n = sh.start(blockIdx.x * kWarps + warp + 1) - s_w;
+    if (lane < 2) sm.cut[lane][warp].unit = -1;
+    if (lane == 0) sm.empty[warp] = n == 0;
+    __syncwarp();
     bool fail = false;
     if (n > 0) {
         const uint64_t policy = policy_evict_first();
-        const int tpp = a.P / kFp4Tile;  // tiles of a page: 1, 2 or 4
-        Pos p = locate(s_w, sm.pre, a, U, lane);
+        const int tshift = a.P == 16 ? 0 : (a.P == 32 ? 1 : 2);  // tiles of a page: 1, 2 or 4
+        Pos p = locate(s_w, bt, lane);
 
-        // window of 32 tiles: lane i holds the pool tile of the share's tile 32 w + i (-1: bad page)
+        // window of 32 steps: lane i holds the pool tiles of the share's step 32 w + i (-1: none)
         Pos wp = p;
-        advance(wp, lane, a, U);
-        auto resolve = [&](long long r) {
-            if (r >= n) return -1;
-            const int phys = __ldg(a.page_table + (size_t)wp.b * a.pt_stride + wp.tile / tpp);
-            if (phys < 0 || phys >= a.num_pages) return -1;
-            return (phys * a.Hk + wp.y / blocks) * tpp + wp.tile % tpp;
+        advance(wp, lane, bt);
+        auto resolve = [&](int r) {
+            int2 t = make_int2(-1, -1);
+            if (r >= n) return t;
+            const int32_t *row = a.page_table + (size_t)wp.b * a.pt_stride;
+            const int t0 = 2 * wp.step, c0 = t0 >> tshift, c1 = (t0 + 1) >> tshift;
+            const bool two = t0 + 1 < (bt.len(wp.b) + kFp4Tile - 1) / kFp4Tile;
+            const int p0 = __ldg(row + c0), p1 = c1 == c0 || !two ? p0 : __ldg(row + c1);
+            const int kvh = blocks == 1 ? wp.y : wp.y / blocks;
+            if (p0 >= 0 && p0 < a.num_pages) t.x = ((p0 * a.Hk + kvh) << tshift) + (t0 & ((1 << tshift) - 1));
+            if (two && p1 >= 0 && p1 < a.num_pages)
+                t.y = ((p1 * a.Hk + kvh) << tshift) + ((t0 + 1) & ((1 << tshift) - 1));
+            // the slot of a bad page is left as it is
+            if (t.x < 0 || (two && t.y < 0)) set_error(a.err, GQA_ERR_BAD_PAGE);
+            return t;
         };
-        auto issue = [&](int idx, int slot) {  // one lane
+        auto issue = [&](int2 t, int slot) {  // one lane
             uint64_t *bar = &sm.full[warp][slot];
-            if (idx < 0) {
-                set_error(a.err, GQA_ERR_BAD_PAGE);
-                mbar_arrive(bar);  // the tile computes on stale data
+            uint8_t(*dst)[CF::kTile] = sm.ring[warp][slot];
+            if (t.x >= 0 && t.y == t.x + 1) {
+                mbar_arrive_expect_tx(bar, 4 * CF::kTile);
+                bulk_load(dst[0], a.k_pages + (size_t)t.x * CF::kTile, 2 * CF::kTile, bar, policy);
+                bulk_load(dst[2], a.v_pages + (size_t)t.x * CF::kTile, 2 * CF::kTile, bar, policy);
                 return;
             }
-            mbar_arrive_expect_tx(bar, 2 * CF::kTile);
-            bulk_load(sm.ring[warp][slot][0], a.k_pages + (size_t)idx * CF::kTile, CF::kTile, bar, policy);
-            bulk_load(sm.ring[warp][slot][1], a.v_pages + (size_t)idx * CF::kTile, CF::kTile, bar, policy);
+            mbar_arrive_expect_tx(bar, ((t.x >= 0) + (t.y >= 0)) * 2 * CF::kTile);
+            if (t.x >= 0) {
+                bulk_load(dst[0], a.k_pages + (size_t)t.x * CF::kTile, CF::kTile, bar, policy);
+                bulk_load(dst[2], a.v_pages + (size_t)t.x * CF::kTile, CF::kTile, bar, policy);
+            }
+            if (t.y >= 0) {
+                bulk_load(dst[1], a.k_pages + (size_t)t.y * CF::kTile, CF::kTile, bar, policy);
+                bulk_load(dst[3], a.v_pages + (size_t)t.y * CF::kTile, CF::kTile, bar, policy);
+            }
         };
-        int win = resolve(lane), next_win = -1;
+        int2 win = resolve(lane), next_win = make_int2(-1, -1);
         if (lane < S && lane < n) issue(win, lane);
         if (n > 32) {
-            advance(wp, 32, a, U);
+            advance(wp, 32, bt);
             next_win = resolve(32 + lane);
         }
 
         State<D, NT> st;
-        bool fresh = true, began = p.tile == 0;
-        int L = 0;
-        int slot = 0;
+        int slot = 0, r = 0;
         uint32_t parity = 0;
-        long long r = 0;
-        for (; r < n; ++r) {
-            const int kvh = p.y / blocks, blk = p.y % blocks;
-            const size_t row0 = (size_t)p.b * a.Hq + kvh * g + blk * hpc;
-            const int nh = min(hpc, g - blk * hpc);
-            if (fresh) {
-                st.reset();
-                L = clamped_len(a, p.b);
-                st.load_q(static_cast<const __nv_bfloat16 *>(a.q) + row0 * D, nh,
-                          a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + kvh) : 1.f), lane);
-                fresh = false;
-            }
-            const bool ok = mbar_wait(&sm.full[warp][slot], parity);
-            if (__any_sync(kFull, !ok)) {
-                fail = true;
-                break;
-            }
-            st.tile(sm.ring[warp][slot][0], sm.ring[warp][slot][1], L - p.tile * kFp4Tile, lane, [&] {
-                const long long ri = r + S;
-                if (ri >= n) return;
-                if ((ri & 31) == 0) {
-                    win = next_win;
-                    if (ri + 32 < n) {
-                        advance(wp, 32, a, U);
-                        next_win = resolve(ri + 32 + lane);
-                    }
+        while (r < n && !fail) {  // a unit, or the part of one that is in the share
+            const Heads hd(a, blocks, hpc, p.b, p.y);
+            st.reset();
+            st.load_q(static_cast<const __nv_bfloat16 *>(a.q) + hd.row0 * D, hd.n,
+                      a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + hd.kvh) : 1.f), lane);
+            int valid = bt.len(p.b) - p.step * kStep;
+            const int end = min(n, r + p.nt - p.step);
+            const bool began = p.step == 0, ended = end - r == p.nt - p.step;
+            const int first = s_w + r - p.step;
+            bool fresh = true;
+            for (; r < end; ++r, valid -= kStep) {
+                const bool ok = mbar_wait(&sm.full[warp][slot], parity);
+                if (__any_sync(kFull, !ok)) {
+                    fail = true;
+                    break;
                 }
-                if (lane == (int)(ri & 31)) issue(win, slot);
-            });
-            if (++slot == S) {
-                slot = 0;
-                parity ^= 1u;
-            }
-            const bool ended = p.tile == p.nt - 1;
-            if (ended || r == n - 1) {
-                st.finish();
-                const int unit = p.b * U + p.y;
-                if (began && ended) {
-                    const float vf = a.v_scale ? __ldg(a.v_scale + kvh) : 1.f;
-                    const int gq = lane >> 2, cq = lane & 3;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int h = nt * 8 + 2 * cq + e;
-                            if (h >= nh) continue;
-#pragma unroll
-                            for (int i = 0; i < CF::C / 4; ++i)
-                                store4(a.out, a.out_f32, (row0 + h) * D + gq * CF::C + 4 * i,
-                                       normalised(make_float4(st.o[nt][2 * i][e], st.o[nt][2 * i][e + 2],
-                                                              st.o[nt][2 * i + 1][e], st.o[nt][2 * i + 1][e + 2]),
-                                                  st.l[nt][e], vf));
-                            if (gq == 0 && a.lse) a.lse[row0 + h] = (st.m[nt][e] + log2f(st.l[nt][e])) * kLn2;
+                st.step(sm.ring[warp][slot][0], valid, fresh, lane, [&] {
+                    const int ri = r + S;
+                    if (ri >= n) return;
+                    if ((ri & 31) == 0) {
+                        win = next_win;
+                        if (ri + 32 < n) {
+                            advance(wp, 32, bt);
+                            next_win = resolve(ri + 32 + lane);
                         }
-                } else if (!began) {
-                    st.dump(sm.head[warp], lane);
-                    head_unit = unit;
-                } else {
-                    // the share ends inside the unit; the ring is free: every copy has been waited for
-                    st.dump(reinterpret_cast<float *>(sm.ring[warp]), lane);
-                    tail_unit = unit;
+                    }
+                    if (lane == (ri & 31)) issue(win, slot);
+                });
+                fresh = false;
+                if (++slot == S) {
+                    slot = 0;
+                    parity ^= 1u;
                 }
-                fresh = began = true;
             }
-            if (r < n - 1) advance(p, 1, a, U);
+            if (fail) break;
+            st.finish();
+            if (began && ended) {
+                const float vf = a.v_scale ? __ldg(a.v_scale + hd.kvh) : 1.f;
+                const int gq = lane >> 2, cq = lane & 3;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int h = nt * 8 + 2 * cq + e;
+                        if (h >= hd.n) continue;
+                        const float r = st.l[nt][e] == 0.f ? 0.f : vf / st.l[nt][e];
+#pragma unroll
+                        for (int i = 0; i < CF::C / 4; ++i)
+                            store4(a.out, a.out_f32, (hd.row0 + h) * D + gq * CF::C + 4 * i,
+                                   make_float4(st.o[nt][2 * i][e] * r, st.o[nt][2 * i][e + 2] * r,
+                                               st.o[nt][2 * i + 1][e] * r, st.o[nt][2 * i + 1][e + 2] * r));
+                        if (gq == 0 && a.lse) a.lse[hd.row0 + h] = (st.m[nt][e] + log2f(st.l[nt][e])) * kLn2;
+                    }
+            } else {
+                // a share that ends inside the unit: the ring is free, every copy has been waited for
+                st.dump(began ? reinterpret_cast<float *>(sm.ring[warp]) : sm.head[warp], lane);
+                if (lane == 0) sm.cut[began ? 1 : 0][warp] = {p.b * U + p.y, first, p.nt};
+            }
+            if (r < n) advance(p, p.nt - p.step, bt);
         }
         if (fail) {
             // give up: no copy may outlive the CTA
@@ -560,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
                 set_error(a.err, GQA_ERR_TIMEOUT);
                 sm.abort_flag = 1;
             }
-            for (long long k = r; k < n && k < r + S; ++k) {
+            for (int k = r; k < n && k < r + S; ++k) {
                 mbar_wait(&sm.full[warp][slot], parity);
                 if (++slot == S) {
                     slot = 0;
@@ -569,133 +637,110 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
             }
         }
     }
-    if (lane == 0) {
-        sm.head_unit[warp] = head_unit;
-        sm.tail_unit[warp] = tail_unit;
-        sm.empty[warp] = n == 0;
-    }
     __syncthreads();
     if (sm.abort_flag) return;
 
-    // ---- units cut between warps.  Task w: the unit that warp w began and did not end; task -1: the
-    // unit that an earlier CTA began.  Its states lie in warp order; each thread owns 4 dims of a head.
-    constexpr int V4 = D / 4;
-    const long long c_start = blockIdx.x * T / NC, c_end = (blockIdx.x + 1) * T / NC;
+    // ---- units cut between warps.  Task w + 1: the unit that warp w began and did not end; task 0:
+    // the unit that an earlier CTA began.  Its states lie in warp order.  Lane t looks task t up; a
+    // warp then merges one head of one task at a time, each lane D / 32 dims.
+    constexpr int V = D / 32;
+    const int c_start = sh.start(blockIdx.x * kWarps), c_end = sh.start((blockIdx.x + 1) * kWarps);
     const int slot_floats = hpc * (D + 2);
-    int open[2] = {-1, -1};  // units that continue in other CTAs: begun before / in this one
-    for (int w = -1; w < kWarps; ++w) {
-        int unit;
-        if (w < 0) {
-            int f = 0;
-            while (sm.empty[f]) ++f;  // some warp of a CTA with work has tiles
-            unit = sm.head_unit[f];
-        } else {
-            unit = sm.tail_unit[w];
-        }
-        if (unit < 0) continue;
-        int w1 = w;  // last warp with a state of the unit
-        for (int k = w + 1; k < kWarps; ++k) {
-            if (sm.empty[k]) continue;
-            if (sm.head_unit[k] != unit) break;
-            w1 = k;
-        }
-        const int b = unit / U, y = unit % U;
-        const int kvh = y / blocks, blk = y % blocks, nh = min(hpc, g - blk * hpc);
-        const size_t row0 = (size_t)b * a.Hq + kvh * g + blk * hpc;
-        // where the unit ends: known to the warp that ended it
-        const int per = (a.B + kRuns - 1) / kRuns;
-        long long us = sm.pre[b / per];
-        for (int k = b / per * per; k < b; ++k) us += tiles_of(clamped_len(a, k));
-        const int nt_b = tiles_of(clamped_len(a, b));
-        us = us * U + (long long)y * nt_b;
-        const bool whole = us >= c_start && us + nt_b <= c_end;
-        const int side = us >= c_start ? 1 : 0;
-        float *piece = a.pieces + ((size_t)blockIdx.x * 2 + side) * slot_floats;
-        const float vf = a.v_scale ? __ldg(a.v_scale + kvh) : 1.f;
-        for (int e = threadIdx.x; e < nh * V4; e += kThreads) {
-            const int h = e / V4, d = (e % V4) * 4;
-            float M = -INFINITY, Ls = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = w < 0 ? 0 : w; k <= w1; ++k) {
+    Cut tc = {-1, 0, 0};
+    int w0 = 0, w1 = 0;  // first and last warp with a state of the unit
+    if (lane <= kWarps) {
+        w0 = max(lane - 1, 0);
+        if (lane == 0)
+            while (sm.empty[w0]) ++w0;  // some warp of a CTA with work has steps
+        tc = sm.cut[lane > 0][w0];
+        w1 = w0;
+        if (tc.unit >= 0)
+            for (int k = w0 + 1; k < kWarps; ++k) {
                 if (sm.empty[k]) continue;
-                const float *s = k == w ? reinterpret_cast<const float *>(sm.ring[k]) : sm.head[k];
-                M = fmaxf(M, s[CF::HW * CF::RS + h]);
+                if (sm.cut[0][k].unit != tc.unit) break;
+                w1 = k;
             }
-            for (int k = w < 0 ? 0 : w; k <= w1; ++k) {
-                if (sm.empty[k]) continue;
-                const float *s = k == w ? reinterpret_cast<const float *>(sm.ring[k]) : sm.head[k];
-                const float f = weight(s[CF::HW * CF::RS + h], M);
-                Ls += f * s[CF::HW * CF::RS + CF::HW + h];
-                add4(acc, f, *reinterpret_cast<const float4 *>(s + h * CF::RS + d));
-            }
-            if (whole) {
-                store4(a.out, a.out_f32, (row0 + h) * D + d, normalised(acc, Ls, vf));
-                if (d == 0 && a.lse) a.lse[row0 + h] = (M + log2f(Ls)) * kLn2;
-            } else {
-                float2 *dst = reinterpret_cast<float2 *>(piece + h * D + d);
-                dst[0] = make_float2(acc.x, acc.y);
-                dst[1] = make_float2(acc.z, acc.w);
-                if (d == 0) {
-                    piece[hpc * D + h] = M;
-                    piece[hpc * D + hpc + h] = Ls;
-                }
-            }
-        }
-        if (!whole) open[side] = unit;
     }
-    if (open[0] < 0 && open[1] < 0) return;
+    // does the unit go on in other CTAs?
+    const bool cross = tc.unit >= 0 && (tc.first < c_start || tc.first + tc.steps > c_end);
+    const unsigned tasks = __ballot_sync(kFull, tc.unit >= 0), crossing = __ballot_sync(kFull, cross);
+    int item = warp;  // the tasks' heads, end to end, are dealt to the warps in turn
+    for (unsigned left = tasks; left; left &= left - 1) {
+        const int t = __ffs(left) - 1;
+        const int unit = __shfl_sync(kFull, tc.unit, t), k0 = __shfl_sync(kFull, w0, t), k1 = __shfl_sync(kFull, w1, t);
+        const Heads hd(a, blocks, hpc, unit / U, unit % U);
+        for (; item < hd.n; item += kWarps) {
+            auto state = [&](int k) { return k == t - 1 ? reinterpret_cast<const float *>(sm.ring[k]) : sm.head[k]; };
+            float M = kNoRef, Ls = 0.f, acc[V] = {};
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k)
+                if (k >= k0 && k <= k1 && !sm.empty[k]) M = fmaxf(M, state(k)[CF::HW * CF::RS + item]);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                if (k < k0 || k > k1 || sm.empty[k]) continue;
+                const float *s = state(k);
+                const float f = ex2_approx(s[CF::HW * CF::RS + item] - M);
+                Ls += f * s[CF::HW * CF::RS + CF::HW + item];
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] += f * s[item * CF::RS + lane * V + i];
+            }
+            if (crossing >> t & 1) {
+                // in the workspace: side 0 of the CTA's pieces is of a unit begun earlier
+                float *piece = a.pieces + ((size_t)blockIdx.x * 2 + (t > 0)) * slot_floats;
+                store_dims<V>(piece, 1, (size_t)item * D + lane * V, acc, 1.f);
+                if (lane == 0) {
+                    piece[hpc * D + item] = M;
+                    piece[hpc * D + hpc + item] = Ls;
+                }
+            } else {
+                put_head<V>(a, hd, item, lane, acc, M, Ls);
+            }
+        }
+        item -= hd.n;
+    }
+    if (!crossing) return;
 
-    // ---- units cut between CTAs: the last to arrive merges the pieces
+    // ---- units cut between CTAs (at most one begun before this one and one in it): the last to
+    // arrive merges the pieces
     __threadfence();
     __syncthreads();
-    if (threadIdx.x < 2) {
-        const int side = threadIdx.x;
+    if (warp == 0 && cross) {
+        const int side = lane > 0, c0 = sh.owner(tc.first) / kWarps, c1 = sh.owner(tc.first + tc.steps - 1) / kWarps;
         int last = 0;
-        if (open[side] >= 0) {
-            const int unit = open[side], b = unit / U, y = unit % U;
-            const int per = (a.B + kRuns - 1) / kRuns;
-            long long us = sm.pre[b / per];
-            for (int k = b / per * per; k < b; ++k) us += tiles_of(clamped_len(a, k));
-            const int nt_b = tiles_of(clamped_len(a, b));
-            us = us * U + (long long)y * nt_b;
-            const int c0 = (int)(((us + 1) * NC + T - 1) / T - 1), c1 = (int)(((us + nt_b) * NC + T - 1) / T - 1);
-            if (atomicAdd(a.counters + unit, 1) == c1 - c0) {
-                a.counters[unit] = 0;  // ready for the next launch
-                last = c1 - c0 + 1;
-                sm.head_unit[side] = c0;
-            }
+        if (atomicAdd(a.counters + tc.unit, 1) == c1 - c0) {
+            a.counters[tc.unit] = 0;  // ready for the next launch
+            last = c1 - c0 + 1;
         }
+        sm.first[side] = c0;
         sm.last[side] = last;
     }
     __syncthreads();
-    for (int side = 0; side < 2; ++side) {
-        const int np = sm.last[side];
+    for (unsigned left = crossing; left; left &= left - 1) {
+        const int t = __ffs(left) - 1, np = sm.last[t > 0], c0 = sm.first[t > 0];
         if (np == 0) continue;
         __threadfence();
-        const int unit = open[side], b = unit / U, y = unit % U;
-        const int kvh = y / blocks, blk = y % blocks, nh = min(hpc, g - blk * hpc);
-        const size_t row0 = (size_t)b * a.Hq + kvh * g + blk * hpc;
-        const float vf = a.v_scale ? __ldg(a.v_scale + kvh) : 1.f;
-        const int c0 = sm.head_unit[side];
+        const int unit = __shfl_sync(kFull, tc.unit, t);
+        const Heads hd(a, blocks, hpc, unit / U, unit % U);
         // the unit begins in its first CTA (side 1) and runs on in the others (side 0)
-        auto piece = [&](int k) { return a.pieces + ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * slot_floats; };
-        for (int e = threadIdx.x; e < nh * V4; e += kThreads) {
-            const int h = e / V4, d = (e % V4) * 4;
-            float M = -INFINITY, Ls = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto piece = [&](int k) { return a.pieces + ((size_t)(c0 + k) * 2 + (k == 0)) * slot_floats; };
+        for (int h = warp; h < hd.n; h += kWarps) {
+            float M = kNoRef, Ls = 0.f, acc[V] = {};
+            for (int k = lane; k < np; k += 32) M = fmaxf(M, __ldcg(piece(k) + hpc * D + h));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
 #pragma unroll 8
-            for (int k = 0; k < np; ++k) M = fmaxf(M, __ldcg(piece(k) + hpc * D + h));
-#pragma unroll 4
             for (int k = 0; k < np; ++k) {
                 const float *s = piece(k);
-                const float f = weight(__ldcg(s + hpc * D + h), M);
+                const float f = ex2_approx(__ldcg(s + hpc * D + h) - M);
                 Ls += f * __ldcg(s + hpc * D + hpc + h);
-                const float2 lo = __ldcg(reinterpret_cast<const float2 *>(s + h * D + d));
-                const float2 hi = __ldcg(reinterpret_cast<const float2 *>(s + h * D + d) + 1);
-                add4(acc, f, make_float4(lo.x, lo.y, hi.x, hi.y));
+#pragma unroll
+                for (int i = 0; i < V; i += 2) {
+                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(s + h * D + lane * V + i));
+                    acc[i] += f * x.x;
+                    acc[i + 1] += f * x.y;
+                }
             }
-            store4(a.out, a.out_f32, (row0 + h) * D + d, normalised(acc, Ls, vf));
-            if (d == 0 && a.lse) a.lse[row0 + h] = (M + log2f(Ls)) * kLn2;
+            put_head<V>(a, hd, h, lane, acc, M, Ls);
         }
     }
 }

@@ -25,7 +25,7 @@ def _decode(fn="gqa_paged_decode", **kw):
 @pytest.mark.parametrize("fn", ["gqa_paged_decode", "gqa_paged_decode_partial"])
 @pytest.mark.parametrize("kw,status", [
     (dict(q=None), -1), (dict(ws=None), -1), (dict(D=96), -2), (dict(P=8), -2), (dict(Hq=6, Hk=4), -2),
-    (dict(npg=1 << 30), -2), (dict(kvd=3), -3), (dict(S=1), -4), (dict(S=64), -4), (dict(S=-2), -4),
+    (dict(npg=1 << 30), -2), (dict(B=65535, pts=1 << 14), -2), (dict(Hq=1 << 30, B=4), -2), (dict(kvd=3), -3), (dict(S=1), -4), (dict(S=64), -4), (dict(S=-2), -4),
     (dict(wsb=256), -5), (dict(ws=_fake(0x10010)), -5), (dict(k=_fake(0x10008)), -9),
     (dict(ks=_fake(0x10002)), -9), (dict(vs=_fake(0x10001)), -9),
 ])
@@ -45,6 +45,7 @@ def test_append_decode_refuses_before_writing():
     assert call(kn=_fake(0x10008)) == -9
     assert call(ks=_fake(0x10002)) == -9
     assert call(D=32) == -2
+    assert call(B=65535, pts=1 << 14) == -2
 
 
 def _write(**kw):
