@@ -105,14 +105,21 @@ def _check(fn: str, status: int):
         raise GQAError(fn, status)
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+# Plain ints, which ctypes converts by the signature: a small decode step is bound by the time
+# this module takes on the host (16.8 -> 9 us a call without c_void_p and Stream objects).
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
@@ -122,10 +129,26 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
         raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if dtype is not None and t.dtype is not dtype and \
+            t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _need_here(*tensors):
+    """All of them (None apart) on the current device, whose stream the call uses."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{here}")
+
+
+def _need_word(workspace: torch.Tensor):
+    """A workspace with room for the error word."""
+    _need(workspace, "workspace", torch.uint8)
+    if workspace.numel() < 256:
+        raise ValueError("workspace must have 256 bytes at least")
 
 
 _KV_DTYPES = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
@@ -223,10 +246,12 @@ def gqa_paged_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
         lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, Hq))
-    need = gqa_paged_decode_workspace_size(B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits)
-    if workspace is None:
-        workspace = new_workspace(need, q.device)
+    if workspace is None:  # (a given one's size is checked by the call)
+        workspace = new_workspace(gqa_paged_decode_workspace_size(
+            B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits), q.device)
     _need(workspace, "workspace", torch.uint8)
+    if kv_dtype == GQA_KV_FP4:
+        _need_here(q, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, out, lse, workspace)
     st = load().gqa_paged_decode(
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), kv_dtype,
         _ptr(page_table), pt_stride, _ptr(seq_lens), B, Hq, Hk, D, P, num_pages, float(scale),
@@ -268,10 +293,13 @@ def gqa_paged_decode_partial(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
     if lse_part is None:
         lse_part = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
     _need(lse_part, "lse_part", torch.float32, (B, Hq))
-    need = gqa_paged_decode_workspace_size(B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits)
-    if workspace is None:
-        workspace = new_workspace(need, q.device)
+    if workspace is None:  # (a given one's size is checked by the call)
+        workspace = new_workspace(gqa_paged_decode_workspace_size(
+            B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits), q.device)
     _need(workspace, "workspace", torch.uint8)
+    if kv_dtype == GQA_KV_FP4:
+        _need_here(q, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, o_part, lse_part,
+                   workspace)
     st = load().gqa_paged_decode_partial(
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), kv_dtype,
         _ptr(page_table), pt_stride, _ptr(seq_lens), B, Hq, Hk, D, P, num_pages, float(scale),
@@ -311,6 +339,8 @@ def gqa_paged_decode_static_scratch(q: torch.Tensor, k_pages: torch.Tensor,
         lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
     _need(out, "out", torch.bfloat16, (B, Hq, D))
     _need(lse, "lse", torch.float32, (B, Hq))
+    if kv_dtype == GQA_KV_FP4:
+        _need_here(q, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, out, lse)
     st = load().gqa_paged_decode_static_scratch(
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), kv_dtype,
         _ptr(page_table), page_table.shape[1], _ptr(seq_lens), B, Hq, Hk, D, P, num_pages,
@@ -333,6 +363,8 @@ def _append_args(k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, 
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B][pt_stride]")
     _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
+    if kv_dtype == GQA_KV_FP4:
+        _need_here(k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale)
     return B, Hk, D, P, num_pages, kv_dtype
 
 
@@ -349,6 +381,9 @@ def gqa_paged_append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch
     if workspace is None:
         workspace = new_workspace(256, k_pages.device)
     _need(workspace, "workspace", torch.uint8)
+    if kv_dtype == GQA_KV_FP4:
+        _need_word(workspace)
+        _need_here(workspace)
     st = load().gqa_paged_append_kv(
         _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
         kv_dtype, _ptr(page_table), page_table.shape[1], _ptr(seq_lens), B, Hk, D, P, num_pages,
@@ -381,10 +416,12 @@ def gqa_paged_append_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.T
         lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, Hq))
-    need = gqa_paged_decode_workspace_size(B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits)
-    if workspace is None:
-        workspace = new_workspace(need, q.device)
+    if workspace is None:  # (a given one's size is checked by the call)
+        workspace = new_workspace(gqa_paged_decode_workspace_size(
+            B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits), q.device)
     _need(workspace, "workspace", torch.uint8)
+    if kv_dtype == GQA_KV_FP4:
+        _need_here(q, out, lse, workspace)
     st = load().gqa_paged_append_decode(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
         _ptr(v_scale), kv_dtype, _ptr(page_table), pt_stride, _ptr(seq_lens), B, Hq, Hk, D, P,
@@ -499,7 +536,8 @@ def gqa_paged_write_kv(k_new: torch.Tensor, v_new: torch.Tensor, cu_q: torch.Ten
     _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
     if workspace is None:
         workspace = new_workspace(256, k_pages.device)
-    _need(workspace, "workspace", torch.uint8)
+    _need_word(workspace)
+    _need_here(k_new, v_new, cu_q, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, workspace)
     if T == 0:
         return workspace
     st = load().gqa_paged_write_kv(
@@ -546,7 +584,9 @@ def gqa_paged_read_kv(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: 
     _need(v_out, "v_out", torch.bfloat16, shape)
     if workspace is None:
         workspace = new_workspace(256, k_pages.device)
-    _need(workspace, "workspace", torch.uint8)
+    _need_word(workspace)
+    _need_here(k_pages, v_pages, page_table, seq_lens, cu_out, starts, k_scale, v_scale, k_out, v_out,
+               workspace)
     if total == 0:
         return k_out, v_out
     st = load().gqa_paged_read_kv(

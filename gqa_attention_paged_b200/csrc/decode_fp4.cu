@@ -7,12 +7,12 @@
 //
 // Schedule.  The 32-token steps of all (sequence, kv head [, block of heads]) units are laid end
 // to end and cut into equal contiguous shares, one per warp of a fixed grid.  A warp streams its
-// share through a private shared-memory ring: the lane that holds a step's page indices issues its
-// bulk copies (a tile's codes and scales are contiguous), the warp waits on the slot's mbarrier,
-// takes the step into registers and hands the slot to the copy of the step kStages further on.  No
-// warp waits for another until the end.  Units cut between the warps of a CTA are then merged
-// through shared memory; those cut between CTAs leave one piece per CTA in the workspace, and the
-// last CTA to arrive merges them, in the order of the CTAs.
+// share through a private shared-memory ring of 16-byte asynchronous copies (a tile's codes and
+// scales are contiguous; a bulk copy per tile, 1152 bytes, was bound by the copies an SM can
+// start, about one in 32 cycles): the step is taken into registers and its slot handed to the step
+// kStages further on.  No warp waits for another until the end.  Units cut between the warps of a
+// CTA are then merged through shared memory; those cut between CTAs leave one piece per CTA in the
+// workspace, and the last CTA to arrive merges them, in the order of the CTAs.
 //
 // Tile.  S^T = K q^T and O^T += V^T P^T on m16n8k16 f16 tensor-core fragments: tokens (dims) are M,
 // 8 packed heads N.  The operands code * scale are exact f16 values; q is bf16 scaled per head by
@@ -52,9 +52,10 @@ struct Cfg {
     static constexpr int kDump = HW * (RS + 2);  // floats: O rows, then m and l
 };
 
-// The unit that a dumped state belongs to: its first step in the batch's order, its steps.
+// The unit that a dumped state belongs to (-1: no state): its first step in the batch's order, its
+// steps, kv head, first row of q and heads.
 struct Cut {
-    int unit, first, steps;
+    int unit, first, steps, kvh, row0, n;
 };
 
 template <int D, int NT>
@@ -62,24 +63,24 @@ struct alignas(128) Smem {
     using C = Cfg<D, NT>;
     uint8_t ring[kWarps][C::kStages][4][C::kTile];  // K, K, V, V; at the end: the state of the unit begun last
     float head[kWarps][C::kDump];                   // the state of a unit begun by an earlier warp
-    uint64_t full[kWarps][C::kStages];
     int pre[kRuns + 1];                             // steps before each run of sequences
     int len[kRuns];                                 // tokens, when a run is one sequence
     int wsum[kWarps];
-    Cut cut[2][kWarps];                             // of head and ring; unit -1: no state
+    Cut cut[2][kWarps];                             // of head and ring
     int empty[kWarps];
-    int abort_flag, last[2], first[2];
+    int last[2], first[2];
     static_assert(sizeof(float) * C::kDump <= sizeof(ring[0]), "a state fits the warp's ring");
 };
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar,
-                                          uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
+// 16 bytes into shared memory, or zeros when `bytes` is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, uint32_t bytes, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(bytes),
+                 "l"(policy)
+                 : "memory");
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -111,6 +112,11 @@ struct Batch {
     __device__ __forceinline__ int steps(int b) const { return steps_of(len(b)); }
 };
 
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+    return x;
+}
 // A step's place: sequence, unit within it (kv head * head blocks + block), step of the unit's nt.
 struct Pos {
     int b, y, step, nt;
@@ -198,47 +204,43 @@ struct State {
         }
     }
 
-    __device__ __forceinline__ void load_q(const __nv_bfloat16 *rows, int nh, float mul, int lane) {
+    // `rows`: the unit's n heads; columns past them repeat the first and are never looked at.
+    __device__ __forceinline__ void load_q(const __nv_bfloat16 *rows, int n, float mul, int lane) {
         const int gq = lane >> 2, cq = lane & 3;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int h = nt * 8 + gq;
-            const bool ok = h < nh;
-            const uint4 *src = reinterpret_cast<const uint4 *>(rows + (size_t)(ok ? h : 0) * D + cq * (D / 4));
-            float x[D / 4];
-            float big = 0.f;
+            const uint4 *src = reinterpret_cast<const uint4 *>(rows + (size_t)(h < n ? h : 0) * D + cq * (D / 4));
+            uint32_t w[D / 8], big = 0;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) unpack_bf16x8(ok ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u), x + 8 * i);
+            for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint4 *>(w + 4 * i) = __ldg(src + i);
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i) big = fmaxf(big, fabsf(x[i]));
-            big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
-            // the head's power of two: the largest |q| into [2^14, 2^15)
-            int e = 0;
-            if (big > 0.f && big < INFINITY) e = 14 - ilogbf(big);
-            e = max(-126, min(126, e));
+            for (int i = 0; i < D / 8; ++i) big = __vmaxu2(big, w[i] & 0x7fff7fffu);
+            big = __vmaxu2(big, __shfl_xor_sync(kFull, big, 1));
+            big = __vmaxu2(big, __shfl_xor_sync(kFull, big, 2));
+            // the head's power of two: the largest |q| into [2^14, 2^15) (none for infinities and NaN)
+            const int ex = max(big >> 16, big & 0xffffu) >> 7, e = ex == 255 ? 0 : min(141 - ex, 126);
             const float up = __int_as_float((127 + e) << 23), down = __int_as_float((127 - e) << 23);
 #pragma unroll
-            for (int ks = 0; ks < C::KS; ++ks) {
-                qf[nt][ks][0] = pack_f16(x[4 * ks] * up, x[4 * ks + 1] * up);
-                qf[nt][ks][1] = pack_f16(x[4 * ks + 2] * up, x[4 * ks + 3] * up);
-            }
+            for (int i = 0; i < D / 8; ++i)
+                qf[nt][i / 2][i & 1] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
             kmul[nt][0] = mul * __shfl_sync(kFull, down, 8 * cq);
             kmul[nt][1] = mul * __shfl_sync(kFull, down, 8 * cq + 4);
         }
     }
 
-    // Fold in a step's two tiles, `valid` tokens of them; `fresh`: the first since reset().  `release`
-    // runs once the step is in registers.
-    template <typename F>
-    __device__ __forceinline__ void step(const uint8_t *slot, int valid, bool fresh, int lane, F release) {
-        constexpr int W = D / 32;  // 32-bit words of a lane's codes per token row / pair
+    static constexpr int W = D / 32;  // 32-bit words of a lane's codes per token row / pair
+    float s[2][NT][4];                // a step's scores per tile
+    uint32_t vr[4][W], vs[4];         // its values and their scales: pairs of tile h in 2 h and 2 h + 1
+
+    // The scores of a step's two tiles; its values into registers.
+    __device__ __forceinline__ void scores(const uint8_t *slot, int lane) {
         const int gq = lane >> 2, cq = lane & 3;
         const uint8_t *kp = slot + gq * (D / 2) + cq * (D / 8);
         const uint8_t *ksp = slot + 8 * D + gq * (D / 16) + (D == 128 ? 2 * cq : cq);
         const uint8_t *vp = slot + 2 * C::kTile + gq * (4 * C::C) + cq * C::C;
         const uint8_t *vsp = slot + 2 * C::kTile + 8 * D + cq * (D / 8) + (gq * C::C / 16) * 2;
-        uint32_t kr[4][W], ks[4], vr[4][W], vs[4];  // rows (pairs) of tile h: 2 h and 2 h + 1
+        uint32_t kr[4][W], ks[4];  // rows of tile h: 2 h and 2 h + 1
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             const int at = (h >> 1) * C::kTile;
@@ -247,8 +249,7 @@ struct State {
             else ks[h] = ksp[at + (h & 1) * (8 * D / 16)] * 0x0101u;
         }
 
-        // ---- scores, a chain per tile
-        float s[2][NT][4];
+        // a chain of products per tile
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -283,9 +284,11 @@ struct State {
             load_words(vr[h], vp + at + (h & 1) * (4 * D));
             vs[h] = *reinterpret_cast<const uint16_t *>(vsp + at + (h & 1) * (4 * D / 8));
         }
-        __syncwarp();
-        release();
+    }
 
+    // Fold the step in, `valid` tokens of it; `fresh`: the first since reset().
+    __device__ __forceinline__ void fold(int valid, bool fresh, int lane) {
+        const int gq = lane >> 2, cq = lane & 3;
         // ---- online softmax in log2 units, scores less the reference; only the steps that move the
         // reference take the column maxima and a rescale
         float top = -INFINITY;
@@ -399,63 +402,41 @@ struct State {
     }
 };
 
-__device__ __forceinline__ void store4(void *out, int f32, size_t idx, float4 v) {
-    if (f32) {
-        reinterpret_cast<float4 *>(out)[idx / 4] = v;
-    } else {
-        reinterpret_cast<uint2 *>(out)[idx / 4] = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-    }
-}
-
-// The V dims at `idx` of a row, times r.
-template <int V>
-__device__ __forceinline__ void store_dims(void *out, int f32, size_t idx, const float (&x)[V], float r) {
+// V consecutive dims of a row at index `idx`, times r.
+template <bool F32, int V>
+__device__ __forceinline__ void store_dims(void *out, size_t idx, const float (&x)[V], float r) {
 #pragma unroll
     for (int i = 0; i < V; i += 2) {
-        if (f32) reinterpret_cast<float2 *>(out)[(idx + i) / 2] = make_float2(x[i] * r, x[i + 1] * r);
+        if (F32) reinterpret_cast<float2 *>(out)[(idx + i) / 2] = make_float2(x[i] * r, x[i + 1] * r);
         else reinterpret_cast<uint32_t *>(out)[(idx + i) / 2] = pack_bf16(x[i] * r, x[i + 1] * r);
     }
 }
 
 // The query heads of unit y of sequence b: kv head, first row of q, heads.
 struct Heads {
-    int kvh, n;
-    size_t row0;
+    int kvh, row0, n;
     __device__ __forceinline__ Heads(const Fp4DecodeArgs &a, int blocks, int hpc, int b, int y) {
         const int g = a.Hq / a.Hk;
         kvh = blocks == 1 ? y : y / blocks;
         const int h0 = (y - kvh * blocks) * hpc;
         n = min(hpc, g - h0);
-        row0 = (size_t)b * a.Hq + kvh * g + h0;
+        row0 = b * a.Hq + kvh * g + h0;
     }
 };
 
-// Lane's V dims of a head from its merged state: O / l times the values' factor; lse.
-template <int V>
-__device__ __forceinline__ void put_head(const Fp4DecodeArgs &a, const Heads &hd, int h, int lane, const float (&o)[V],
-                                         float m, float l) {
-    const float vf = a.v_scale ? __ldg(a.v_scale + hd.kvh) : 1.f;
-    store_dims<V>(a.out, a.out_f32, (hd.row0 + h) * (32 * V) + lane * V, o, l == 0.f ? 0.f : vf / l);
-    if (lane == 0 && a.lse) a.lse[hd.row0 + h] = (m + log2f(l)) * kLn2;
-}
-
-template <int D, int NT>
+template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
     decode_fp4_kernel(const Fp4DecodeArgs a, const int hpc, const int blocks) {
     using CF = Cfg<D, NT>;
-    constexpr int S = CF::kStages;
+    constexpr int S = CF::kStages, V = D / 32;
     extern __shared__ uint8_t smem_raw[];
     Smem<D, NT> &sm = *reinterpret_cast<Smem<D, NT> *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int U = a.Hk * blocks;
     const Batch bt = {a, sm.pre, sm.len, U, a.B <= kRuns ? 1 : (a.B + kRuns - 1) / kRuns};
 
-    if (lane < S) mbar_init(&sm.full[warp][lane], 1);
-    if (threadIdx.x == 0) sm.abort_flag = 0;
-    fence_barrier_init();
-    fence_proxy_async_smem();
-    // launched with programmatic stream serialization: everything above may overlap the previous
-    // kernel of the stream, nothing below reads or writes before that kernel is complete
+    // launched with programmatic stream serialization: nothing below reads or writes before the
+    // previous kernel of the stream is complete
     grid_dependency_wait();
     grid_dependents_launch();
 
@@ -463,15 +444,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
     int none = 0;  // a sequence without tokens?
     {
         const int b0 = min(a.B, (int)threadIdx.x * bt.per), b1 = min(a.B, b0 + bt.per);
-        int sum = 0;
+        int incl = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int L0 = __ldg(a.seq_lens + b), L = clamped(a, L0);
             if (L != L0 && blockIdx.x == 0) set_error(a.err, GQA_ERR_BAD_PAGE);
             if (bt.per == 1) sm.len[b] = L;
-            sum += steps_of(L);
+            incl += steps_of(L);
             none |= L == 0;
         }
-        int incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int t = __shfl_up_sync(kFull, incl, o);
@@ -488,12 +469,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
     const int T = U * sm.pre[kRuns];
 
     if (none) {  // zeros and -inf
+        const float zero[4] = {};
+#pragma unroll 1
         for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
             if (bt.len(b) != 0) continue;
-            for (int e = threadIdx.x; e < a.Hq * D / 4; e += kThreads)
-                store4(a.out, a.out_f32, (size_t)b * a.Hq * D + 4 * e, make_float4(0.f, 0.f, 0.f, 0.f));
-            if (a.lse)
-                for (int e = threadIdx.x; e < a.Hq; e += kThreads) a.lse[(size_t)b * a.Hq + e] = -INFINITY;
+#pragma unroll 1
+            for (int e = threadIdx.x; e < a.Hq * D / 4; e += kThreads) {
+                store_dims<F32>(a.out, (size_t)b * a.Hq * D + 4 * e, zero, 0.f);
+                if (a.lse && e % (D / 4) == 0) a.lse[(size_t)b * a.Hq + e / (D / 4)] = -INFINITY;
+            }
         }
     }
     // CTAs with work
@@ -509,94 +493,77 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
     if (lane < 2) sm.cut[lane][warp].unit = -1;
     if (lane == 0) sm.empty[warp] = n == 0;
     __syncwarp();
-    bool fail = false;
     if (n > 0) {
         const uint64_t policy = policy_evict_first();
         const int tshift = a.P == 16 ? 0 : (a.P == 32 ? 1 : 2);  // tiles of a page: 1, 2 or 4
         Pos p = locate(s_w, bt, lane);
-
-        // window of 32 steps: lane i holds the pool tiles of the share's step 32 w + i (-1: none)
+        // window of 32 steps: lane i holds the place and the pool tiles of the share's step 32 w + i
+        // (-1: none)
         Pos wp = p;
-        advance(wp, lane, bt);
-        auto resolve = [&](int r) {
-            int2 t = make_int2(-1, -1);
-            if (r >= n) return t;
-            const int32_t *row = a.page_table + (size_t)wp.b * a.pt_stride;
-            const int t0 = 2 * wp.step, c0 = t0 >> tshift, c1 = (t0 + 1) >> tshift;
-            const bool two = t0 + 1 < (bt.len(wp.b) + kFp4Tile - 1) / kFp4Tile;
-            const int p0 = __ldg(row + c0), p1 = c1 == c0 || !two ? p0 : __ldg(row + c1);
-            const int kvh = blocks == 1 ? wp.y : wp.y / blocks;
-            if (p0 >= 0 && p0 < a.num_pages) t.x = ((p0 * a.Hk + kvh) << tshift) + (t0 & ((1 << tshift) - 1));
-            if (two && p1 >= 0 && p1 < a.num_pages)
-                t.y = ((p1 * a.Hk + kvh) << tshift) + ((t0 + 1) & ((1 << tshift) - 1));
-            // the slot of a bad page is left as it is
-            if (t.x < 0 || (two && t.y < 0)) set_error(a.err, GQA_ERR_BAD_PAGE);
-            return t;
+        int2 win = make_int2(-1, -1);
+
+        const uint32_t ring = smem_u32(sm.ring[warp][0][0]) + lane * 16;
+        auto ask = [&](int i) {  // step i of the share; a group of copies for every i
+            if (i < n) {
+                if ((i & 31) == 0) {
+                    advance(wp, i == 0 ? lane : 32, bt);
+                    win = make_int2(-1, -1);
+                    if (i + lane < n) {
+                        const int32_t *row = a.page_table + (size_t)wp.b * a.pt_stride;
+                        const int t0 = 2 * wp.step, c0 = t0 >> tshift, c1 = (t0 + 1) >> tshift;
+                        const bool two = t0 + 1 < (bt.len(wp.b) + kFp4Tile - 1) / kFp4Tile;
+                        const int p0 = __ldg(row + c0), p1 = c1 == c0 || !two ? p0 : __ldg(row + c1);
+                        const int kvh = blocks == 1 ? wp.y : wp.y / blocks;
+                        if (p0 >= 0 && p0 < a.num_pages) win.x = ((p0 * a.Hk + kvh) << tshift) + (t0 & ((1 << tshift) - 1));
+                        if (two && p1 >= 0 && p1 < a.num_pages)
+                            win.y = ((p1 * a.Hk + kvh) << tshift) + ((t0 + 1) & ((1 << tshift) - 1));
+                        // a bad page reads as zeros
+                        if (win.x < 0 || (two && win.y < 0)) set_error(a.err, GQA_ERR_BAD_PAGE);
+                    }
+                }
+                const uint32_t slot = ring + (i & (S - 1)) * (4 * CF::kTile);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int t = __shfl_sync(kFull, h ? win.y : win.x, i & 31);
+                    const size_t at = (size_t)max(t, 0) * CF::kTile + lane * 16;
+                    const uint32_t bytes = t < 0 ? 0 : 16;
+#pragma unroll
+                    for (int c = 0; c < CF::kTile; c += 512) {
+                        if (c + 512 > CF::kTile && lane * 16 >= CF::kTile - c) continue;
+                        copy16(slot + h * CF::kTile + c, a.k_pages + at + c, bytes, policy);
+                        copy16(slot + (2 + h) * CF::kTile + c, a.v_pages + at + c, bytes, policy);
+                    }
+                }
+            }
+            copies_commit();
         };
-        auto issue = [&](int2 t, int slot) {  // one lane
-            uint64_t *bar = &sm.full[warp][slot];
-            uint8_t(*dst)[CF::kTile] = sm.ring[warp][slot];
-            if (t.x >= 0 && t.y == t.x + 1) {
-                mbar_arrive_expect_tx(bar, 4 * CF::kTile);
-                bulk_load(dst[0], a.k_pages + (size_t)t.x * CF::kTile, 2 * CF::kTile, bar, policy);
-                bulk_load(dst[2], a.v_pages + (size_t)t.x * CF::kTile, 2 * CF::kTile, bar, policy);
-                return;
-            }
-            mbar_arrive_expect_tx(bar, ((t.x >= 0) + (t.y >= 0)) * 2 * CF::kTile);
-            if (t.x >= 0) {
-                bulk_load(dst[0], a.k_pages + (size_t)t.x * CF::kTile, CF::kTile, bar, policy);
-                bulk_load(dst[2], a.v_pages + (size_t)t.x * CF::kTile, CF::kTile, bar, policy);
-            }
-            if (t.y >= 0) {
-                bulk_load(dst[1], a.k_pages + (size_t)t.y * CF::kTile, CF::kTile, bar, policy);
-                bulk_load(dst[3], a.v_pages + (size_t)t.y * CF::kTile, CF::kTile, bar, policy);
-            }
-        };
-        int2 win = resolve(lane), next_win = make_int2(-1, -1);
-        if (lane < S && lane < n) issue(win, lane);
-        if (n > 32) {
-            advance(wp, 32, bt);
-            next_win = resolve(32 + lane);
-        }
+#pragma unroll 1
+        for (int i = 0; i < S; ++i) ask(i);
 
         State<D, NT> st;
-        int slot = 0, r = 0;
-        uint32_t parity = 0;
-        while (r < n && !fail) {  // a unit, or the part of one that is in the share
-            const Heads hd(a, blocks, hpc, p.b, p.y);
-            st.reset();
-            st.load_q(static_cast<const __nv_bfloat16 *>(a.q) + hd.row0 * D, hd.n,
-                      a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + hd.kvh) : 1.f), lane);
-            int valid = bt.len(p.b) - p.step * kStep;
-            const int end = min(n, r + p.nt - p.step);
-            const bool began = p.step == 0, ended = end - r == p.nt - p.step;
-            const int first = s_w + r - p.step;
-            bool fresh = true;
-            for (; r < end; ++r, valid -= kStep) {
-                const bool ok = mbar_wait(&sm.full[warp][slot], parity);
-                if (__any_sync(kFull, !ok)) {
-                    fail = true;
-                    break;
-                }
-                st.step(sm.ring[warp][slot][0], valid, fresh, lane, [&] {
-                    const int ri = r + S;
-                    if (ri >= n) return;
-                    if ((ri & 31) == 0) {
-                        win = next_win;
-                        if (ri + 32 < n) {
-                            advance(wp, 32, bt);
-                            next_win = resolve(ri + 32 + lane);
-                        }
-                    }
-                    if (lane == (ri & 31)) issue(win, slot);
-                });
-                fresh = false;
-                if (++slot == S) {
-                    slot = 0;
-                    parity ^= 1u;
-                }
+        Heads hd(a, blocks, hpc, 0, 0);
+        bool fresh = true, began = p.step == 0;
+        int valid = 0;
+#pragma unroll 1
+        for (int r = 0; r < n; ++r) {
+            if (fresh) {
+                hd = Heads(a, blocks, hpc, p.b, p.y);
+                valid = bt.len(p.b) - p.step * kStep;
+                st.reset();
+                st.load_q(static_cast<const __nv_bfloat16 *>(a.q) + (size_t)hd.row0 * D, hd.n,
+                          a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + hd.kvh) : 1.f), lane);
             }
-            if (fail) break;
+            copies_wait<S - 1>();
+            __syncwarp();
+            st.scores(sm.ring[warp][r & (S - 1)][0], lane);
+            __syncwarp();  // the slot is in registers
+            ask(r + S);
+            st.fold(valid, fresh, lane);
+            fresh = false;
+            valid -= kStep;
+            const bool ended = ++p.step == p.nt;
+            if (!ended && r < n - 1) continue;
+            // ---- the end of a unit, or of the share
             st.finish();
             if (began && ended) {
                 const float vf = a.v_scale ? __ldg(a.v_scale + hd.kvh) : 1.f;
@@ -607,150 +574,155 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
                     for (int e = 0; e < 2; ++e) {
                         const int h = nt * 8 + 2 * cq + e;
                         if (h >= hd.n) continue;
-                        const float r = st.l[nt][e] == 0.f ? 0.f : vf / st.l[nt][e];
+                        float x[CF::C];
 #pragma unroll
-                        for (int i = 0; i < CF::C / 4; ++i)
-                            store4(a.out, a.out_f32, (hd.row0 + h) * D + gq * CF::C + 4 * i,
-                                   make_float4(st.o[nt][2 * i][e] * r, st.o[nt][2 * i][e + 2] * r,
-                                               st.o[nt][2 * i + 1][e] * r, st.o[nt][2 * i + 1][e + 2] * r));
+                        for (int d = 0; d < CF::C; ++d) x[d] = st.o[nt][d / 2][e + 2 * (d & 1)];
+                        store_dims<F32>(a.out, (size_t)(hd.row0 + h) * D + gq * CF::C, x,
+                                        st.l[nt][e] == 0.f ? 0.f : vf / st.l[nt][e]);
                         if (gq == 0 && a.lse) a.lse[hd.row0 + h] = (st.m[nt][e] + log2f(st.l[nt][e])) * kLn2;
                     }
             } else {
-                // a share that ends inside the unit: the ring is free, every copy has been waited for
+                // a share that ends inside the unit: the ring is free, no copy is in flight
                 st.dump(began ? reinterpret_cast<float *>(sm.ring[warp]) : sm.head[warp], lane);
-                if (lane == 0) sm.cut[began ? 1 : 0][warp] = {p.b * U + p.y, first, p.nt};
+                if (lane == 0) sm.cut[began][warp] = {p.b * U + p.y, s_w + r + 1 - p.step, p.nt, hd.kvh, hd.row0, hd.n};
             }
-            if (r < n) advance(p, p.nt - p.step, bt);
-        }
-        if (fail) {
-            // give up: no copy may outlive the CTA
-            if (lane == 0) {
-                set_error(a.err, GQA_ERR_TIMEOUT);
-                sm.abort_flag = 1;
-            }
-            for (int k = r; k < n && k < r + S; ++k) {
-                mbar_wait(&sm.full[warp][slot], parity);
-                if (++slot == S) {
-                    slot = 0;
-                    parity ^= 1u;
-                }
+            fresh = began = true;
+            if (r == n - 1) break;
+            p.step = 0;  // on to the next unit
+            if (++p.y == U) {
+                p.y = 0;
+                do p.nt = bt.steps(++p.b);
+                while (p.nt == 0);
             }
         }
     }
     __syncthreads();
-    if (sm.abort_flag) return;
 
     // ---- units cut between warps.  Task w + 1: the unit that warp w began and did not end; task 0:
     // the unit that an earlier CTA began.  Its states lie in warp order.  Lane t looks task t up; a
     // warp then merges one head of one task at a time, each lane D / 32 dims.
-    constexpr int V = D / 32;
     const int c_start = sh.start(blockIdx.x * kWarps), c_end = sh.start((blockIdx.x + 1) * kWarps);
     const int slot_floats = hpc * (D + 2);
-    Cut tc = {-1, 0, 0};
-    int w0 = 0, w1 = 0;  // first and last warp with a state of the unit
+    Cut tc = {-1, 0, 0, 0, 0, 0};
+    unsigned has = 0;  // the warps that have a state of it
     if (lane <= kWarps) {
-        w0 = max(lane - 1, 0);
+        int w0 = max(lane - 1, 0);
         if (lane == 0)
             while (sm.empty[w0]) ++w0;  // some warp of a CTA with work has steps
         tc = sm.cut[lane > 0][w0];
-        w1 = w0;
-        if (tc.unit >= 0)
-            for (int k = w0 + 1; k < kWarps; ++k) {
-                if (sm.empty[k]) continue;
-                if (sm.cut[0][k].unit != tc.unit) break;
-                w1 = k;
-            }
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k)
+            if (k > w0 && sm.cut[0][k].unit == tc.unit) has |= 1u << k;
+        has |= 1u << w0;
     }
     // does the unit go on in other CTAs?
     const bool cross = tc.unit >= 0 && (tc.first < c_start || tc.first + tc.steps > c_end);
-    const unsigned tasks = __ballot_sync(kFull, tc.unit >= 0), crossing = __ballot_sync(kFull, cross);
-    int item = warp;  // the tasks' heads, end to end, are dealt to the warps in turn
-    for (unsigned left = tasks; left; left &= left - 1) {
-        const int t = __ffs(left) - 1;
-        const int unit = __shfl_sync(kFull, tc.unit, t), k0 = __shfl_sync(kFull, w0, t), k1 = __shfl_sync(kFull, w1, t);
-        const Heads hd(a, blocks, hpc, unit / U, unit % U);
-        for (; item < hd.n; item += kWarps) {
-            auto state = [&](int k) { return k == t - 1 ? reinterpret_cast<const float *>(sm.ring[k]) : sm.head[k]; };
-            float M = kNoRef, Ls = 0.f, acc[V] = {};
+    const unsigned crossing = __ballot_sync(kFull, cross);
+    auto put = [&](int row, int kvh, const float(&acc)[V], float M, float L) {
+        const float vf = a.v_scale ? __ldg(a.v_scale + kvh) : 1.f;
+        store_dims<F32>(a.out, (size_t)row * D + lane * V, acc, L == 0.f ? 0.f : vf / L);
+        if (lane == 0 && a.lse) a.lse[row] = (M + log2f(L)) * kLn2;
+    };
+    int h = warp;  // the tasks' heads, end to end, are dealt to the warps in turn
+#pragma unroll 1
+    for (unsigned left = __ballot_sync(kFull, tc.unit >= 0); left; left &= left - 1) {
+        const int t = __ffs(left) - 1, heads = __shfl_sync(kFull, tc.n, t);
+        const int row0 = __shfl_sync(kFull, tc.row0, t), kvh = __shfl_sync(kFull, tc.kvh, t);
+        const unsigned of = __shfl_sync(kFull, has, t);
+#pragma unroll 1
+        for (; h < heads; h += kWarps) {
+            auto state = [&](int w) { return w == t - 1 ? reinterpret_cast<const float *>(sm.ring[w]) : sm.head[w]; };
+            const bool there = of >> lane & 1;
+            const float m = there ? state(lane & (kWarps - 1))[CF::HW * CF::RS + h] : kNoRef;
+            const float M = warp_max(m), f = there ? ex2_approx(m - M) : 0.f;
+            float L = 0.f, acc[V] = {};
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k)
-                if (k >= k0 && k <= k1 && !sm.empty[k]) M = fmaxf(M, state(k)[CF::HW * CF::RS + item]);
+            for (int w = 0; w < kWarps; ++w) {
+                const float fw = __shfl_sync(kFull, f, w);
+                if (!(of >> w & 1)) continue;
+                const float *s = state(w);
+                L += fw * s[CF::HW * CF::RS + CF::HW + h];
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                if (k < k0 || k > k1 || sm.empty[k]) continue;
-                const float *s = state(k);
-                const float f = ex2_approx(s[CF::HW * CF::RS + item] - M);
-                Ls += f * s[CF::HW * CF::RS + CF::HW + item];
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[i] += f * s[item * CF::RS + lane * V + i];
+                for (int i = 0; i < V; ++i) acc[i] += fw * s[h * CF::RS + lane * V + i];
             }
             if (crossing >> t & 1) {
-                // in the workspace: side 0 of the CTA's pieces is of a unit begun earlier
+                // a CTA's pieces: of the unit begun earlier, and of the one begun in it
                 float *piece = a.pieces + ((size_t)blockIdx.x * 2 + (t > 0)) * slot_floats;
-                store_dims<V>(piece, 1, (size_t)item * D + lane * V, acc, 1.f);
+                store_dims<true>(piece, (size_t)h * D + lane * V, acc, 1.f);
                 if (lane == 0) {
-                    piece[hpc * D + item] = M;
-                    piece[hpc * D + hpc + item] = Ls;
+                    piece[hpc * D + h] = M;
+                    piece[hpc * D + hpc + h] = L;
                 }
             } else {
-                put_head<V>(a, hd, item, lane, acc, M, Ls);
+                put(row0 + h, kvh, acc, M, L);
             }
         }
-        item -= hd.n;
+        h -= heads;
     }
     if (!crossing) return;
 
     // ---- units cut between CTAs (at most one begun before this one and one in it): the last to
     // arrive merges the pieces
-    __threadfence();
     __syncthreads();
     if (warp == 0 && cross) {
         const int side = lane > 0, c0 = sh.owner(tc.first) / kWarps, c1 = sh.owner(tc.first + tc.steps - 1) / kWarps;
+        __threadfence();
         int last = 0;
         if (atomicAdd(a.counters + tc.unit, 1) == c1 - c0) {
             a.counters[tc.unit] = 0;  // ready for the next launch
             last = c1 - c0 + 1;
         }
+        __threadfence();
         sm.first[side] = c0;
         sm.last[side] = last;
     }
     __syncthreads();
+#pragma unroll 1
     for (unsigned left = crossing; left; left &= left - 1) {
         const int t = __ffs(left) - 1, np = sm.last[t > 0], c0 = sm.first[t > 0];
         if (np == 0) continue;
-        __threadfence();
-        const int unit = __shfl_sync(kFull, tc.unit, t);
-        const Heads hd(a, blocks, hpc, unit / U, unit % U);
-        // the unit begins in its first CTA (side 1) and runs on in the others (side 0)
+        const int heads = __shfl_sync(kFull, tc.n, t), row0 = __shfl_sync(kFull, tc.row0, t);
+        const int kvh = __shfl_sync(kFull, tc.kvh, t);
+        // begun in the unit's first CTA (piece 1), carried on in the others (piece 0)
         auto piece = [&](int k) { return a.pieces + ((size_t)(c0 + k) * 2 + (k == 0)) * slot_floats; };
-        for (int h = warp; h < hd.n; h += kWarps) {
-            float M = kNoRef, Ls = 0.f, acc[V] = {};
-            for (int k = lane; k < np; k += 32) M = fmaxf(M, __ldcg(piece(k) + hpc * D + h));
+#pragma unroll 1
+        for (h = warp; h < heads; h += kWarps) {
+            float M = kNoRef, L = 0.f, acc[V] = {};
+#pragma unroll 1
+            for (int c = 0; c < np; c += 32) {
+                const bool there = c + lane < np;
+                const float *mine = piece(there ? c + lane : c) + hpc * D + h;
+                const float m = there ? __ldcg(mine) : kNoRef, l = __ldcg(mine + hpc);
+                const float up = fmaxf(M, warp_max(m)), f = there ? ex2_approx(m - up) : 0.f, keep = ex2_approx(M - up);
+                M = up;
+                L *= keep;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-#pragma unroll 8
-            for (int k = 0; k < np; ++k) {
-                const float *s = piece(k);
-                const float f = ex2_approx(__ldcg(s + hpc * D + h) - M);
-                Ls += f * __ldcg(s + hpc * D + hpc + h);
+                for (int i = 0; i < V; ++i) acc[i] *= keep;
+                const int end = min(32, np - c);
+#pragma unroll 4
+                for (int j = 0; j < end; ++j) {
+                    const float fj = __shfl_sync(kFull, f, j);
+                    L += fj * __shfl_sync(kFull, l, j);
+                    const float *s = piece(c + j) + h * D + lane * V;
 #pragma unroll
-                for (int i = 0; i < V; i += 2) {
-                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(s + h * D + lane * V + i));
-                    acc[i] += f * x.x;
-                    acc[i + 1] += f * x.y;
+                    for (int i = 0; i < V; i += 2) {
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(s + i));
+                        acc[i] += fj * x.x;
+                        acc[i + 1] += fj * x.y;
+                    }
                 }
             }
-            put_head<V>(a, hd, h, lane, acc, M, Ls);
+            put(row0 + h, kvh, acc, M, L);
         }
     }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool F32>
 cudaError_t launch_t(const Fp4DecodeArgs &a, cudaStream_t stream) {
     const int g = a.Hq / a.Hk;
     const int hpc = a.pack_gqa ? (g < 8 * NT ? g : 8 * NT) : 1;
     const size_t smem = sizeof(Smem<D, NT>) + 128;
-    auto kern = decode_fp4_kernel<D, NT>;
+    auto kern = decode_fp4_kernel<D, NT, F32>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
@@ -776,8 +748,12 @@ size_t fp4_decode_piece_bytes(int Hq, int Hk, int D) {
 
 cudaError_t launch_decode_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {
     const bool wide = a.pack_gqa && a.Hq / a.Hk > 8;
-    if (a.D == 128) return wide ? launch_t<128, 2>(a, stream) : launch_t<128, 1>(a, stream);
-    return wide ? launch_t<64, 2>(a, stream) : launch_t<64, 1>(a, stream);
+    if (a.out_f32) {
+        if (a.D == 128) return wide ? launch_t<128, 2, true>(a, stream) : launch_t<128, 1, true>(a, stream);
+        return wide ? launch_t<64, 2, true>(a, stream) : launch_t<64, 1, true>(a, stream);
+    }
+    if (a.D == 128) return wide ? launch_t<128, 2, false>(a, stream) : launch_t<128, 1, false>(a, stream);
+    return wide ? launch_t<64, 2, false>(a, stream) : launch_t<64, 1, false>(a, stream);
 }
 
 }  // namespace gqa
