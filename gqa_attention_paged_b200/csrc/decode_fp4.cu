@@ -82,6 +82,18 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// Not volatile: the products of a step's scores and of the step before run in one another's gaps.
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t d;
     asm("mul.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -274,7 +286,7 @@ struct State {
                     const uint32_t af[4] = {hmul2(ha[2 * k], sc[2 * h][blk]), hmul2(hb[2 * k], sc[2 * h + 1][blk]),
                                             hmul2(ha[2 * k + 1], sc[2 * h][blk]), hmul2(hb[2 * k + 1], sc[2 * h + 1][blk])};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(s[h][nt], af, qf[nt][2 * i + k][0], qf[nt][2 * i + k][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma(s[h][nt], af, qf[nt][2 * i + k][0], qf[nt][2 * i + k][1]);
                 }
             }
         }
@@ -345,8 +357,8 @@ struct State {
                 for (int e = 0; e < 4; ++e) p[e] = ex2_approx(s[h][nt][e]);
                 l[nt][0] += p[0] + p[2];
                 l[nt][1] += p[1] + p[3];
-                pb[h][nt][0] = movmatrix_trans(pack_f16(p[0], p[1]));
-                pb[h][nt][1] = movmatrix_trans(pack_f16(p[2], p[3]));
+                pb[h][nt][0] = transpose8x8(pack_f16(p[0], p[1]));
+                pb[h][nt][1] = transpose8x8(pack_f16(p[2], p[3]));
             }
 
         // ---- O^T += V^T P^T
@@ -363,7 +375,7 @@ struct State {
                     const uint32_t af[4] = {hmul2(ha[2 * k], va), hmul2(ha[2 * k + 1], va), hmul2(hb[2 * k], vb),
                                             hmul2(hb[2 * k + 1], vb)};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * i + k], af, pb[h][nt][0], pb[h][nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma(o[nt][2 * i + k], af, pb[h][nt][0], pb[h][nt][1]);
                 }
             }
         }
