@@ -33,23 +33,21 @@ constexpr float kLn2 = 0.6931471805599453f;
 // when a score passes it by kLazyRef: weights stay below 2^15, inside f16, and the largest is at
 // least 2^kRefBelow, so that f16's subnormal step costs a small weight 2^-32 of the largest.
 constexpr float kRefBelow = 7.0f, kLazyRef = 15.0f;
+constexpr int kCtasPerSm = 2;
+constexpr int kHeads = 8;  // packed heads of a unit at most: the columns of a product
 constexpr float kNoRef = -3e38f;  // below every reference
 constexpr int kStep = 2 * kFp4Tile;  // tokens of a step: two tiles
-constexpr int kMinSteps = 2;         // steps per warp below which fewer CTAs work
+constexpr int kMinSteps = 1;         // steps per warp below which fewer CTAs work
 constexpr int kRuns = kThreads;      // the sequences' step prefix is kept per run of ceil(B / kRuns)
 
-template <int NT>
-constexpr int ctas_per_sm() { return NT == 1 ? 2 : 1; }
-
-template <int D, int NT>
+template <int D>
 struct Cfg {
     static constexpr int KS = D / 16;         // k steps of the scores, 16-dim tiles of the output
     static constexpr int C = D / 8;           // dims of a lane's V codes
     static constexpr int kTile = fp4_tile_bytes(D);
     static constexpr int kStages = D == 128 ? 2 : 4;
-    static constexpr int HW = 8 * NT;         // packed head columns
     static constexpr int RS = D + 4;          // padded row of a dumped state
-    static constexpr int kDump = HW * (RS + 2);  // floats: O rows, then m and l
+    static constexpr int kDump = kHeads * (RS + 2);  // floats: O rows, then m and l
 };
 
 // The unit that a dumped state belongs to (-1: no state): its first step in the batch's order, its
@@ -58,9 +56,9 @@ struct Cut {
     int unit, first, steps, kvh, row0, n;
 };
 
-template <int D, int NT>
+template <int D>
 struct alignas(128) Smem {
-    using C = Cfg<D, NT>;
+    using C = Cfg<D>;
     uint8_t ring[kWarps][C::kStages][4][C::kTile];  // K, K, V, V; at the end: the state of the unit begun last
     float head[kWarps][C::kDump];                   // the state of a unit begun by an earlier warp
     int pre[kRuns + 1];                             // steps before each run of sequences
@@ -87,6 +85,11 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     uint32_t d;
@@ -199,80 +202,62 @@ struct Shares {
 };
 
 // One warp's attention over part of a unit: lane (gq = lane / 4, cq = lane % 4).
-template <int D, int NT>
+template <int D>
 struct State {
-    using C = Cfg<D, NT>;
-    uint32_t qf[NT][C::KS][2];   // q^T fragments: head 8 nt + gq, dims (D / 4) cq + 4 ks ..
-    float kmul[NT][2];           // to log2 units, for heads 8 nt + 2 cq and + 1
-    float o[NT][C::KS][4];       // dims gq C + 2 dt (e = 0, 1) and + 1 (e = 2, 3); heads 2 cq + (e & 1)
-    float m[NT][2], l[NT][2];
+    using C = Cfg<D>;
+    static constexpr int W = D / 32;  // 32-bit words of a lane's codes per token row / pair
+    uint32_t qf[C::KS][2];            // q^T fragments: head gq, dims (D / 4) cq + 4 ks ..
+    float kmul[2];                    // to log2 units, for heads 2 cq and + 1
+    float o[C::KS][4];                // dims gq C + 2 dt (e = 0, 1) and + 1 (e = 2, 3); heads 2 cq + (e & 1)
+    float m[2], l[2];
+    float s[2][4];                    // a step's scores per tile: products, then exponents
+    uint32_t vr[4][W], vs[4];         // its values and their scales: pairs of tile h in 2 h and 2 h + 1
 
     __device__ __forceinline__ void reset() {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int dt = 0; dt < C::KS; ++dt) o[nt][dt][0] = o[nt][dt][1] = o[nt][dt][2] = o[nt][dt][3] = 0.f;
-            m[nt][0] = m[nt][1] = l[nt][0] = l[nt][1] = 0.f;
-        }
+        for (int dt = 0; dt < C::KS; ++dt) o[dt][0] = o[dt][1] = o[dt][2] = o[dt][3] = 0.f;
+        m[0] = m[1] = l[0] = l[1] = 0.f;
     }
 
     // `rows`: the unit's n heads; columns past them repeat the first and are never looked at.
     __device__ __forceinline__ void load_q(const __nv_bfloat16 *rows, int n, float mul, int lane) {
         const int gq = lane >> 2, cq = lane & 3;
+        const uint4 *src = reinterpret_cast<const uint4 *>(rows + (size_t)(gq < n ? gq : 0) * D + cq * (D / 4));
+        uint32_t w[D / 8], big = 0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int h = nt * 8 + gq;
-            const uint4 *src = reinterpret_cast<const uint4 *>(rows + (size_t)(h < n ? h : 0) * D + cq * (D / 4));
-            uint32_t w[D / 8], big = 0;
+        for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint4 *>(w + 4 * i) = __ldg(src + i);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint4 *>(w + 4 * i) = __ldg(src + i);
+        for (int i = 0; i < D / 8; ++i) big = __vmaxu2(big, w[i] & 0x7fff7fffu);
+        big = __vmaxu2(big, __shfl_xor_sync(kFull, big, 1));
+        big = __vmaxu2(big, __shfl_xor_sync(kFull, big, 2));
+        // the head's power of two: the largest |q| into [2^14, 2^15) (none for infinities and NaN)
+        const int ex = max(big >> 16, big & 0xffffu) >> 7, e = ex == 255 ? 0 : min(141 - ex, 126);
+        const float up = __int_as_float((127 + e) << 23), down = __int_as_float((127 - e) << 23);
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) big = __vmaxu2(big, w[i] & 0x7fff7fffu);
-            big = __vmaxu2(big, __shfl_xor_sync(kFull, big, 1));
-            big = __vmaxu2(big, __shfl_xor_sync(kFull, big, 2));
-            // the head's power of two: the largest |q| into [2^14, 2^15) (none for infinities and NaN)
-            const int ex = max(big >> 16, big & 0xffffu) >> 7, e = ex == 255 ? 0 : min(141 - ex, 126);
-            const float up = __int_as_float((127 + e) << 23), down = __int_as_float((127 - e) << 23);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-                qf[nt][i / 2][i & 1] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
-            kmul[nt][0] = mul * __shfl_sync(kFull, down, 8 * cq);
-            kmul[nt][1] = mul * __shfl_sync(kFull, down, 8 * cq + 4);
-        }
+        for (int i = 0; i < D / 8; ++i)
+            qf[i / 2][i & 1] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+        kmul[0] = mul * __shfl_sync(kFull, down, 8 * cq);
+        kmul[1] = mul * __shfl_sync(kFull, down, 8 * cq + 4);
     }
 
-    static constexpr int W = D / 32;  // 32-bit words of a lane's codes per token row / pair
-    float s[2][NT][4];                // a step's scores per tile
-    uint32_t vr[4][W], vs[4];         // its values and their scales: pairs of tile h in 2 h and 2 h + 1
-
-    // The scores of a step's two tiles; its values into registers.
+    // The products q k of a step's two tiles; its values into registers.
     __device__ __forceinline__ void scores(const uint8_t *slot, int lane) {
         const int gq = lane >> 2, cq = lane & 3;
         const uint8_t *kp = slot + gq * (D / 2) + cq * (D / 8);
         const uint8_t *ksp = slot + 8 * D + gq * (D / 16) + (D == 128 ? 2 * cq : cq);
         const uint8_t *vp = slot + 2 * C::kTile + gq * (4 * C::C) + cq * C::C;
         const uint8_t *vsp = slot + 2 * C::kTile + 8 * D + cq * (D / 8) + (gq * C::C / 16) * 2;
-        uint32_t kr[4][W], ks[4];  // rows of tile h: 2 h and 2 h + 1
+        uint32_t kr[4][W], sc[4][2];  // rows of tile h in 2 h and 2 h + 1; their scales, twice each
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             const int at = (h >> 1) * C::kTile;
             load_words(kr[h], kp + at + (h & 1) * (8 * D / 2));
-            if constexpr (D == 128) ks[h] = *reinterpret_cast<const uint16_t *>(ksp + at + (h & 1) * (8 * D / 16));
-            else ks[h] = ksp[at + (h & 1) * (8 * D / 16)] * 0x0101u;
+            const uint8_t *two = ksp + at + (h & 1) * (8 * D / 16);
+            const uint32_t x = e4m3x2_to_f16(D == 128 ? *reinterpret_cast<const uint16_t *>(two) : *two * 0x0101u);
+            sc[h][0] = __byte_perm(x, x, 0x1010);
+            sc[h][1] = __byte_perm(x, x, 0x3232);
         }
-
         // a chain of products per tile
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) s[h][nt][0] = s[h][nt][1] = s[h][nt][2] = s[h][nt][3] = 0.f;
-        uint32_t sc[4][2];
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            const uint32_t two = e4m3x2_to_f16(ks[h]);
-            sc[h][0] = __byte_perm(two, two, 0x1010);
-            sc[h][1] = __byte_perm(two, two, 0x3232);
-        }
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             const int blk = i / 2;  // 16 dims
@@ -285,8 +270,8 @@ struct State {
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t af[4] = {hmul2(ha[2 * k], sc[2 * h][blk]), hmul2(hb[2 * k], sc[2 * h + 1][blk]),
                                             hmul2(ha[2 * k + 1], sc[2 * h][blk]), hmul2(hb[2 * k + 1], sc[2 * h + 1][blk])};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma(s[h][nt], af, qf[nt][2 * i + k][0], qf[nt][2 * i + k][1]);
+                    if (i + k == 0) mma_first(s[h], af, qf[0][0], qf[0][1]);
+                    else mma(s[h], af, qf[2 * i + k][0], qf[2 * i + k][1]);
                 }
             }
         }
@@ -303,63 +288,59 @@ struct State {
         const int gq = lane >> 2, cq = lane & 3;
         // ---- online softmax in log2 units, scores less the reference; only the steps that move the
         // reference take the column maxima and a rescale
-        float top = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[h][e] = fmaf(s[h][e], kmul[e & 1], -m[e & 1]);
         if (valid < kStep) {  // what follows the sequence may be anything: its scores and scales go
+            __syncwarp();     // (keeps this a branch: 113 -> 109.5 us at batch 256)
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 if (2 * cq + 8 * h >= valid) vs[h] = 0u;
                 if (2 * cq + 8 * h + 1 >= valid) vs[h] &= 0xffu;
+                if (gq + 8 * h >= valid) s[h >> 1][2 * (h & 1)] = s[h >> 1][2 * (h & 1) + 1] = -INFINITY;
             }
         }
+        float top = -INFINITY;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[h][nt][e] = fmaf(s[h][nt][e], kmul[nt][e & 1], -m[nt][e & 1]);
-                    if (valid < kStep && gq + 8 * (2 * h + (e >> 1)) >= valid) s[h][nt][e] = -INFINITY;
-                    top = fmaxf(top, s[h][nt][e]);
-                }
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, s[h][e]);
         if (__any_sync(kFull, top > kLazyRef || fresh)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(fmaxf(s[0][e], s[0][e + 2]), fmaxf(s[1][e], s[1][e + 2]));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
+                // 0 where the head's reference stays; it may begin anywhere
+                const float up = fresh ? mx - kRefBelow : fmaxf(mx - kRefBelow, 0.f);
+                const float alpha = fresh ? 1.f : ex2_approx(-up);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(fmaxf(s[0][nt][e], s[0][nt][e + 2]), fmaxf(s[1][nt][e], s[1][nt][e + 2]));
-                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 16));
-                    // 0 where the head's reference stays; it may begin anywhere
-                    const float up = fresh ? mx - kRefBelow : fmaxf(mx - kRefBelow, 0.f);
-                    const float alpha = fresh ? 1.f : ex2_approx(-up);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        s[h][nt][e] -= up;
-                        s[h][nt][e + 2] -= up;
-                    }
-                    m[nt][e] += up;
-                    l[nt][e] *= alpha;
-#pragma unroll
-                    for (int dt = 0; dt < C::KS; ++dt) {
-                        o[nt][dt][e] *= alpha;
-                        o[nt][dt][e + 2] *= alpha;
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    s[h][e] -= up;
+                    s[h][e + 2] -= up;
                 }
-        }
-        uint32_t pb[2][NT][2];
+                m[e] += up;
+                l[e] *= alpha;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float p[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) p[e] = ex2_approx(s[h][nt][e]);
-                l[nt][0] += p[0] + p[2];
-                l[nt][1] += p[1] + p[3];
-                pb[h][nt][0] = transpose8x8(pack_f16(p[0], p[1]));
-                pb[h][nt][1] = transpose8x8(pack_f16(p[2], p[3]));
+                for (int dt = 0; dt < C::KS; ++dt) {
+                    o[dt][e] *= alpha;
+                    o[dt][e + 2] *= alpha;
+                }
             }
+        }
+        uint32_t pb[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = ex2_approx(s[h][e]);
+            l[0] += p[0] + p[2];
+            l[1] += p[1] + p[3];
+            pb[h][0] = transpose8x8(pack_f16(p[0], p[1]));
+            pb[h][1] = transpose8x8(pack_f16(p[2], p[3]));
+        }
 
         // ---- O^T += V^T P^T
 #pragma unroll
@@ -374,8 +355,7 @@ struct State {
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t af[4] = {hmul2(ha[2 * k], va), hmul2(ha[2 * k + 1], va), hmul2(hb[2 * k], vb),
                                             hmul2(hb[2 * k + 1], vb)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma(o[nt][2 * i + k], af, pb[h][nt][0], pb[h][nt][1]);
+                    mma(o[2 * i + k], af, pb[h][0], pb[h][1]);
                 }
             }
         }
@@ -384,33 +364,27 @@ struct State {
     // Sum l over the lanes that share a head column.
     __device__ __forceinline__ void finish() {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float v = l[nt][e];
-                v += __shfl_xor_sync(kFull, v, 4);
-                v += __shfl_xor_sync(kFull, v, 8);
-                v += __shfl_xor_sync(kFull, v, 16);
-                l[nt][e] = v;
-            }
+        for (int e = 0; e < 2; ++e) {
+            l[e] += __shfl_xor_sync(kFull, l[e], 4);
+            l[e] += __shfl_xor_sync(kFull, l[e], 8);
+            l[e] += __shfl_xor_sync(kFull, l[e], 16);
+        }
     }
 
     __device__ __forceinline__ void dump(float *dst, int lane) const {
         const int gq = lane >> 2, cq = lane & 3;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int e = 0; e < 2; ++e) {
+            const int h = 2 * cq + e;
+            float4 *row = reinterpret_cast<float4 *>(dst + h * C::RS + gq * C::C);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int h = nt * 8 + 2 * cq + e;
-                float4 *row = reinterpret_cast<float4 *>(dst + h * C::RS + gq * C::C);
-#pragma unroll
-                for (int i = 0; i < C::C / 4; ++i)
-                    row[i] = make_float4(o[nt][2 * i][e], o[nt][2 * i][e + 2], o[nt][2 * i + 1][e], o[nt][2 * i + 1][e + 2]);
-                if (gq == 0) {
-                    dst[C::HW * C::RS + h] = m[nt][e];
-                    dst[C::HW * C::RS + C::HW + h] = l[nt][e];
-                }
+            for (int i = 0; i < C::C / 4; ++i)
+                row[i] = make_float4(o[2 * i][e], o[2 * i][e + 2], o[2 * i + 1][e], o[2 * i + 1][e + 2]);
+            if (gq == 0) {
+                dst[kHeads * C::RS + h] = m[e];
+                dst[kHeads * C::RS + kHeads + h] = l[e];
             }
+        }
     }
 };
 
@@ -436,13 +410,13 @@ struct Heads {
     }
 };
 
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
+template <int D, bool F32>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_fp4_kernel(const Fp4DecodeArgs a, const int hpc, const int blocks) {
-    using CF = Cfg<D, NT>;
+    using CF = Cfg<D>;
     constexpr int S = CF::kStages, V = D / 32;
     extern __shared__ uint8_t smem_raw[];
-    Smem<D, NT> &sm = *reinterpret_cast<Smem<D, NT> *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    Smem<D> &sm = *reinterpret_cast<Smem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int U = a.Hk * blocks;
     const Batch bt = {a, sm.pre, sm.len, U, a.B <= kRuns ? 1 : (a.B + kRuns - 1) / kRuns};
@@ -549,10 +523,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
             }
             copies_commit();
         };
+        State<D> st;
+        {
+            const Heads h0(a, blocks, hpc, p.b, p.y);
+            st.load_q(static_cast<const __nv_bfloat16 *>(a.q) + (size_t)h0.row0 * D, h0.n,
+                      a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + h0.kvh) : 1.f), lane);
+        }
 #pragma unroll 1
         for (int i = 0; i < S; ++i) ask(i);
-
-        State<D, NT> st;
         Heads hd(a, blocks, hpc, 0, 0);
         bool fresh = true, began = p.step == 0;
         int valid = 0;
@@ -562,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
                 hd = Heads(a, blocks, hpc, p.b, p.y);
                 valid = bt.len(p.b) - p.step * kStep;
                 st.reset();
-                st.load_q(static_cast<const __nv_bfloat16 *>(a.q) + (size_t)hd.row0 * D, hd.n,
+                if (r > 0) st.load_q(static_cast<const __nv_bfloat16 *>(a.q) + (size_t)hd.row0 * D, hd.n,
                           a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + hd.kvh) : 1.f), lane);
             }
             copies_wait<S - 1>();
@@ -581,18 +559,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
                 const float vf = a.v_scale ? __ldg(a.v_scale + hd.kvh) : 1.f;
                 const int gq = lane >> 2, cq = lane & 3;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int e = 0; e < 2; ++e) {
+                    const int h = 2 * cq + e;
+                    if (h >= hd.n) continue;
+                    float x[CF::C];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int h = nt * 8 + 2 * cq + e;
-                        if (h >= hd.n) continue;
-                        float x[CF::C];
-#pragma unroll
-                        for (int d = 0; d < CF::C; ++d) x[d] = st.o[nt][d / 2][e + 2 * (d & 1)];
-                        store_dims<F32>(a.out, (size_t)(hd.row0 + h) * D + gq * CF::C, x,
-                                        st.l[nt][e] == 0.f ? 0.f : vf / st.l[nt][e]);
-                        if (gq == 0 && a.lse) a.lse[hd.row0 + h] = (st.m[nt][e] + log2f(st.l[nt][e])) * kLn2;
-                    }
+                    for (int d = 0; d < CF::C; ++d) x[d] = st.o[d / 2][e + 2 * (d & 1)];
+                    store_dims<F32>(a.out, (size_t)(hd.row0 + h) * D + gq * CF::C, x, st.l[e] == 0.f ? 0.f : vf / st.l[e]);
+                    if (gq == 0 && a.lse) a.lse[hd.row0 + h] = (st.m[e] + log2f(st.l[e])) * kLn2;
+                }
             } else {
                 // a share that ends inside the unit: the ring is free, no copy is in flight
                 st.dump(began ? reinterpret_cast<float *>(sm.ring[warp]) : sm.head[warp], lane);
@@ -645,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
         for (; h < heads; h += kWarps) {
             auto state = [&](int w) { return w == t - 1 ? reinterpret_cast<const float *>(sm.ring[w]) : sm.head[w]; };
             const bool there = of >> lane & 1;
-            const float m = there ? state(lane & (kWarps - 1))[CF::HW * CF::RS + h] : kNoRef;
+            const float m = there ? state(lane & (kWarps - 1))[kHeads * CF::RS + h] : kNoRef;
             const float M = warp_max(m), f = there ? ex2_approx(m - M) : 0.f;
             float L = 0.f, acc[V] = {};
 #pragma unroll
@@ -653,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
                 const float fw = __shfl_sync(kFull, f, w);
                 if (!(of >> w & 1)) continue;
                 const float *s = state(w);
-                L += fw * s[CF::HW * CF::RS + CF::HW + h];
+                L += fw * s[kHeads * CF::RS + kHeads + h];
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[i] += fw * s[h * CF::RS + lane * V + i];
             }
@@ -729,19 +704,19 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<NT>())
     }
 }
 
-template <int D, int NT, bool F32>
+template <int D, bool F32>
 cudaError_t launch_t(const Fp4DecodeArgs &a, cudaStream_t stream) {
     const int g = a.Hq / a.Hk;
-    const int hpc = a.pack_gqa ? (g < 8 * NT ? g : 8 * NT) : 1;
-    const size_t smem = sizeof(Smem<D, NT>) + 128;
-    auto kern = decode_fp4_kernel<D, NT, F32>;
+    const int hpc = a.pack_gqa ? (g < kHeads ? g : kHeads) : 1;
+    const size_t smem = sizeof(Smem<D>) + 128;
+    auto kern = decode_fp4_kernel<D, F32>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.sms * ctas_per_sm<NT>());
+    cfg.gridDim = dim3(a.sms * kCtasPerSm);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -752,20 +727,15 @@ cudaError_t launch_t(const Fp4DecodeArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
-// Two pieces per CTA of the largest grid, each a state of up to 16 heads.
+// Two pieces per CTA of the largest grid.
 size_t fp4_decode_piece_bytes(int Hq, int Hk, int D) {
-    const int g = Hq / Hk, hpc = g < 16 ? g : 16;
-    return (size_t)kStreamMaxSms * 2 * 2 * hpc * (D + 2) * sizeof(float);
+    const int g = Hq / Hk, hpc = g < kHeads ? g : kHeads;
+    return (size_t)kStreamMaxSms * kCtasPerSm * 2 * hpc * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_decode_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {
-    const bool wide = a.pack_gqa && a.Hq / a.Hk > 8;
-    if (a.out_f32) {
-        if (a.D == 128) return wide ? launch_t<128, 2, true>(a, stream) : launch_t<128, 1, true>(a, stream);
-        return wide ? launch_t<64, 2, true>(a, stream) : launch_t<64, 1, true>(a, stream);
-    }
-    if (a.D == 128) return wide ? launch_t<128, 2, false>(a, stream) : launch_t<128, 1, false>(a, stream);
-    return wide ? launch_t<64, 2, false>(a, stream) : launch_t<64, 1, false>(a, stream);
+    if (a.D == 128) return a.out_f32 ? launch_t<128, true>(a, stream) : launch_t<128, false>(a, stream);
+    return a.out_f32 ? launch_t<64, true>(a, stream) : launch_t<64, false>(a, stream);
 }
 
 }  // namespace gqa
