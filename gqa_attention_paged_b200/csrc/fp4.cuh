@@ -65,6 +65,12 @@ __device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
     return r & 0xffu;
 }
 
+__device__ __forceinline__ uint32_t f32_to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // Four pairs of fp32 values -> four bytes of e2m1 codes (nearest, ties to even, saturating at
 // 6), lo[i] in the low nibble of byte i.
 __device__ __forceinline__ uint32_t f32_to_e2m1x8(const float (&lo)[4], const float (&hi)[4]) {
@@ -93,6 +99,43 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4 &w, float *x) {
     }
 }
 
+// x / s for many bf16 values x over one s, in fp32, as good as rounded correctly to any use that
+// rounds it to e4m3 or e2m1: with r = RN(1 / s) and q = RN(x r), RN(q - (q s - x) r) in 3 operations
+// instead of a division's dozen and its slow path.
+//   The correction's remainder is exact, so the result is RN(y) of a y within 2^-47 of x / s.  It can
+//   be another neighbour than RN(x / s) only if x / s is within 2^-47 of the middle of two fp32 values,
+//   and that changes a code only if one of these is a tie T of the codes, T = t / 16 with t <= 31 up to
+//   a power of two.  With S the 24-bit integer of s and x' the integer x in its unit (a multiple of
+//   2^16), that is |t S / 16 - x'| = S 2^-24 up to 2^-22.  The left side is a multiple of 1 / 16, so S is
+//   within 4 of some k 2^20, 8 <= k <= 15, say S = k 2^20 + d; then t S / 16 = t k 2^16 + t d / 16 and
+//   t d = +-k.  For odd t >= 17 no d does that (t d = 0 or at least 17), and an even t is a smaller one
+//   over a smaller power of two, with the same S: e2m1's ties 5, 7, 3 and 1 over 4, 2 or 1, for which
+//   the left side is a multiple of 1 / 4 and so k is 8 or 12: 5 d, 7 d, 3 d, d over 4 are not k / 16.
+// fits(): whether the steps stay in the normal range for |x| <= m; if not the caller divides.
+struct Quotient {
+    float s, minus_r;
+    __device__ __forceinline__ explicit Quotient(float s_) : s(s_), minus_r(-1.f / s_) {}
+    __device__ __forceinline__ bool fits(float m) const { return s >= 0x1p-60f && s <= 0x1p60f && m < 0x1p20f * s; }
+    __device__ __forceinline__ float operator()(float x) const {
+        const float q = x * -minus_r;
+        return fmaf(fmaf(q, s, -x), minus_r, q);  // (a zero keeps its sign)
+    }
+};
+static __device__ __noinline__ float divide(float x, float s) { return x / s; }
+
+// 32 bytes: one 256-bit store where the address allows it, which `wide` says.
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        uint4 *d = static_cast<uint4 *>(dst);
+        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // Index of the sequence whose run of rows holds row r: the last b with cu[b] <= r, in
 // [0, B - 1] whatever cu holds.
 template <typename T>
@@ -100,10 +143,35 @@ __device__ __forceinline__ int sequence_of(const T *cu, int B, long long r) {
     int lo = 0, hi = B - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((long long)__ldg(cu + mid) <= r) lo = mid;
+        if ((long long)cu[mid] <= r) lo = mid;
         else hi = mid - 1;
     }
     return lo;
 }
+
+// The first rows and lengths of a batch: a copy in shared memory for up to kMax sequences, so that a
+// row's search costs one trip to memory and not one per level; the caller's arrays beyond.
+template <typename T>
+struct Sequences {
+    static constexpr int kMax = 256;
+    T cu_s[kMax + 1];
+    int len_s[kMax];
+    const T *cu;
+    const int32_t *lens;
+
+    // By all threads of the CTA; a barrier has to follow.
+    __device__ __forceinline__ void load(const T *cu_g, const int32_t *lens_g, int B) {
+        const bool here = B <= kMax;
+        if (threadIdx.x == 0) {
+            cu = here ? cu_s : cu_g;
+            lens = here ? len_s : lens_g;
+        }
+        if (!here) return;
+        for (int b = threadIdx.x; b <= B; b += blockDim.x) {
+            if (cu_g) cu_s[b] = __ldg(cu_g + b);
+            if (b < B) len_s[b] = __ldg(lens_g + b);
+        }
+    }
+};
 
 }  // namespace gqa

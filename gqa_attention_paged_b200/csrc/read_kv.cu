@@ -4,135 +4,189 @@
 // pools' own layout (what a kernel that takes bf16 pages then runs on).
 //
 // A value is code * scale (exact) * factor in fp32, rounded once to bf16.  Bound by HBM: 4-bit
-// in, 16-bit out.  One thread per (token, kv head, 16 dims).
+// or 8-bit in, 16-bit out.  A CTA takes a run of output rows: first a thread per row finds the
+// row's place in the pool (the page table is read once per row, not once per element), then a
+// warp takes 16 rows of one kv head at a time, a lane 16 dims of a row at once: all its loads
+// go out before the first conversion, and every store is a whole 32-byte sector.
 #include "fp4.cuh"
 #include "quant_kv.h"
 
 namespace gqa {
 namespace {
 
-__device__ __forceinline__ void store_bf16x16(uint16_t *dst, const float (&x)[16]) {
-    uint32_t w[8];
+constexpr int kThreads = 256;
+constexpr int kMaxRows = 128;  // output rows of a CTA
+constexpr int kGroup = 16;     // rows a warp takes at a time
+
+// Eight f16x2 -> 16 values times g as bf16.
+__device__ __forceinline__ void scaled_bf16(const uint32_t (&h)[8], float g, uint32_t (&w)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
-    uint4 *d = reinterpret_cast<uint4 *>(dst);
-    d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        w[i] = pack_bf16(f.x * g, f.y * g);
+    }
 }
 
-__device__ __forceinline__ void f16x2_to_f32(uint32_t h, float &lo, float &hi) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    lo = f.x;
-    hi = f.y;
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
+    const __half2 d = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&d);
 }
 
-// 16 dims (block c) of one token's K row.
-template <int D>
-__device__ __forceinline__ void read_fp4_k(const uint8_t *tile, int tok, int c, float g, float (&x)[16]) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(tile + tok * (D / 2) + c * 8));
-    const float s = e4m3_to_f32(__ldg(tile + 8 * D + tok * (D / 16) + c));
-    const uint32_t u[2] = {w.x, w.y};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t h[4];
-        e2m1x8_to_f16(u[i], h);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            f16x2_to_f32(h[k], x[8 * i + 2 * k], x[8 * i + 2 * k + 1]);
-            x[8 * i + 2 * k] = x[8 * i + 2 * k] * s * g;
-            x[8 * i + 2 * k + 1] = x[8 * i + 2 * k + 1] * s * g;
+// The raw bytes of 16 dims (block c) of one cached row, keys or values.
+template <int KIND>
+struct Raw {
+    uint4 a, b;
+    float s;
+    uint32_t sc;
+};
+
+// `q`: the row's index in the pool, ((page * Hk + kv head) * P + slot).
+template <int KIND, int D, bool IS_V>
+__device__ __forceinline__ void fetch(Raw<KIND> &x, const void *pages, const float *scale, int q, int c, int pshift) {
+    if constexpr (KIND == GQA_KV_BF16) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(pages) + (size_t)q * D + c * 16);
+        x.a = __ldg(p);
+        x.b = __ldg(p + 1);
+    } else if constexpr (KIND == GQA_KV_FP8_E4M3) {
+        x.a = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(pages) + (size_t)q * D + c * 16));
+        x.s = __ldg(scale + (q >> pshift));
+    } else {
+        const uint8_t *tile = static_cast<const uint8_t *>(pages) + (size_t)(q / kFp4Tile) * fp4_tile_bytes(D);
+        const int tok = q % kFp4Tile;
+        if constexpr (!IS_V) {
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(tile + tok * (D / 2) + c * 8));
+            x.a.x = w.x;
+            x.a.y = w.y;
+            x.sc = __ldg(tile + 8 * D + tok * (D / 16) + c);
+        } else {
+            // both tokens of the pair; the other one's row reads the same bytes
+            constexpr int C = D / 8;
+            const int pair = tok / 2;
+            const uint8_t *codes = tile + (pair >> 2) * (4 * D) + (pair & 3) * C;
+            if constexpr (C == 16) {
+                x.a = __ldg(reinterpret_cast<const uint4 *>(codes + c * (4 * C)));
+            } else {
+                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(codes + (2 * c) * (4 * C)));
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(codes + (2 * c + 1) * (4 * C)));
+                x.a = make_uint4(u.x, u.y, v.x, v.y);
+            }
+            x.sc = __ldg(tile + 8 * D + pair * (D / 8) + c * 2 + (tok & 1));
         }
     }
 }
 
-// The same of its V row: the token's nibble of 16 bytes.
-template <int D>
-__device__ __forceinline__ void read_fp4_v(const uint8_t *tile, int tok, int c, float g, float (&x)[16]) {
-    constexpr int C = D / 8;
-    const int pair = tok / 2;
-    const uint8_t *codes = tile + (pair >> 2) * (4 * D) + (pair & 3) * C;
-    const float s = e4m3_to_f32(__ldg(tile + 8 * D + pair * (D / 8) + c * 2 + (tok & 1)));
+template <int KIND, bool IS_V>
+__device__ __forceinline__ void convert(const Raw<KIND> &x, int q, float g, uint32_t (&w)[8]) {
+    if constexpr (KIND == GQA_KV_BF16) {
+        const uint32_t u[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int d = c * 16 + 4 * i;
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(codes + (d / C) * (4 * C) + d % C));
-        uint32_t h[4];
-        e2m1x8_to_f16(w, h);
+        for (int i = 0; i < 8; ++i) w[i] = u[i];
+    } else if constexpr (KIND == GQA_KV_FP8_E4M3) {
+        const uint32_t u[4] = {x.a.x, x.a.y, x.a.z, x.a.w};
+        uint32_t h[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            float lo, hi;
-            f16x2_to_f32(h[k], lo, hi);
-            x[4 * i + k] = ((tok & 1) ? hi : lo) * s * g;
+        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(u[i], h[2 * i], h[2 * i + 1]);
+        scaled_bf16(h, x.s, w);
+    } else {
+        const uint32_t one = e4m3x2_to_f16(x.sc), sc = __byte_perm(one, one, 0x1010);
+        uint32_t h[8];
+        if constexpr (!IS_V) {
+            const uint32_t u[2] = {x.a.x, x.a.y};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                uint32_t t[4];
+                e2m1x8_to_f16(u[i], t);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h[4 * i + k] = t[k];
+            }
+        } else {
+            // this token's nibbles of 16 bytes, gathered into 8 bytes
+            const uint32_t u[4] = {x.a.x, x.a.y, x.a.z, x.a.w};
+            const int shift = (q & 1) * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t n = (u[i] >> shift) & 0x0f0f0f0fu;  // 0a 0b 0c 0d
+                const uint32_t m = (n | (n >> 4)) & 0x00ff00ffu;   // ba in byte 0, dc in byte 2
+                uint32_t t[4];
+                e2m1x8_to_f16(m, t);
+                h[2 * i] = t[0];
+                h[2 * i + 1] = t[2];
+            }
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = f16x2_mul(h[i], sc);
+        scaled_bf16(h, g, w);
     }
 }
 
 template <int KIND, int D>
-__global__ void __launch_bounds__(256) read_kv_kernel(const ReadArgs a) {
-    constexpr int G = D / 16;
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const int c = (int)(i % G), j = (int)(i / G % a.Hk);
-    const long long r = i / G / a.Hk;  // output row, or slot of the output pages
-    const long long unit = a.paged ? r / a.P : r;
-    if (unit >= a.total) return;
-    const int b = sequence_of(a.cu_out, a.B, unit);
-    const long long u0 = __ldg(a.cu_out + b), u1 = __ldg(a.cu_out + b + 1);
-    if (unit < u0 || unit >= u1) return;
-    const int L = __ldg(a.seq_lens + b), s0 = a.starts ? __ldg(a.starts + b) : 0;
-    if (L < 0 || L > a.pt_stride * a.P || s0 < 0) {
-        set_error(a.err, GQA_ERR_BAD_PAGE);
-        return;
-    }
-    const long long t = a.paged ? (s0 / a.P + (unit - u0)) * a.P + r % a.P : s0 + (unit - u0);
-    if (t < s0 || t >= L) {
-        // a page's slots outside the stretch are no error, a row past the sequence is
-        if (!a.paged || t / a.P > (L - 1) / a.P || L == 0) set_error(a.err, GQA_ERR_BAD_PAGE);
-        return;
-    }
-    const int phys = __ldg(a.page_table + (size_t)b * a.pt_stride + t / a.P);
-    if (phys < 0 || phys >= a.num_pages) {
-        set_error(a.err, GQA_ERR_BAD_PAGE);
-        return;
-    }
-    const int slot = (int)(t % a.P);
-    const size_t dst = (a.paged ? ((size_t)unit * a.Hk + j) * a.P + slot : (size_t)unit * a.Hk + j) * D + c * 16;
-    uint16_t *ko = static_cast<uint16_t *>(a.k_out) + dst, *vo = static_cast<uint16_t *>(a.v_out) + dst;
-    const size_t row = (((size_t)phys * a.Hk + j) * a.P + slot) * D + c * 16;
-    if constexpr (KIND == GQA_KV_BF16) {
-        const uint4 *k = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.k_pages) + row);
-        const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.v_pages) + row);
-        const uint4 k0 = __ldg(k), k1 = __ldg(k + 1), v0 = __ldg(v), v1 = __ldg(v + 1);
-        reinterpret_cast<uint4 *>(ko)[0] = k0;
-        reinterpret_cast<uint4 *>(ko)[1] = k1;
-        reinterpret_cast<uint4 *>(vo)[0] = v0;
-        reinterpret_cast<uint4 *>(vo)[1] = v1;
-    } else if constexpr (KIND == GQA_KV_FP8_E4M3) {
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(kv ? a.v_pages : a.k_pages) + row));
-            const float s = __ldg((kv ? a.v_scale : a.k_scale) + (size_t)phys * a.Hk + j);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-            float x[16];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t h0, h1;
-                e4m3x4_to_f16x4(u[e], h0, h1);
-                f16x2_to_f32(h0, x[4 * e], x[4 * e + 1]);
-                f16x2_to_f32(h1, x[4 * e + 2], x[4 * e + 3]);
+__global__ void __launch_bounds__(kThreads) read_kv_kernel(const ReadArgs a, const int rows, const long long total_rows,
+                                                           const int pshift, const bool wide) {
+    constexpr int G = D / 16, kAt = 32 / G, kIts = kGroup / kAt;  // rows of a warp at once, and how often
+    __shared__ int place[kMaxRows];
+    __shared__ Sequences<int64_t> seqs;
+    const long long r0 = (long long)blockIdx.x * rows;
+    const int P = 1 << pshift;
+    grid_dependency_wait();
+    grid_dependents_launch();
+
+    // ---- where the CTA's rows lie in the pool (head 0; -1: not read)
+    seqs.load(a.cu_out, a.seq_lens, a.B);
+    __syncthreads();
+    if (threadIdx.x < rows) {
+        const long long r = r0 + threadIdx.x;
+        int at = -1;
+        if (r < total_rows) {
+            const long long unit = a.paged ? r >> pshift : r;
+            const int b = sequence_of(seqs.cu, a.B, unit);
+            const long long u0 = seqs.cu[b], u1 = seqs.cu[b + 1];
+            const int L = seqs.lens[b], s0 = a.starts ? __ldg(a.starts + b) : 0;
+            if (unit >= u0 && unit < u1) {
+                const bool ok = L >= 0 && L <= a.pt_stride * P && s0 >= 0;
+                const long long t = a.paged ? (((s0 >> pshift) + (unit - u0)) << pshift) + (r & (P - 1)) : s0 + (unit - u0);
+                if (ok && t >= s0 && t < L) {
+                    const int phys = __ldg(a.page_table + (size_t)b * a.pt_stride + (t >> pshift));
+                    if (phys >= 0 && phys < a.num_pages) at = phys * a.Hk * P + (int)(t & (P - 1));
+                    else set_error(a.err, GQA_ERR_BAD_PAGE);
+                } else if (!ok || !a.paged || L == 0 || (t >> pshift) > ((L - 1) >> pshift)) {
+                    // (a page's slots outside the stretch are no error)
+                    set_error(a.err, GQA_ERR_BAD_PAGE);
+                }
             }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] *= s;
-            store_bf16x16(kv ? vo : ko, x);
         }
-    } else {
-        const size_t tile = fp4_tile_offset(phys, a.Hk, j, a.P, slot, D);
-        float x[16];
-        read_fp4_k<D>(static_cast<const uint8_t *>(a.k_pages) + tile, slot % kFp4Tile, c,
-                      a.k_scale ? __ldg(a.k_scale + j) : 1.f, x);
-        store_bf16x16(ko, x);
-        read_fp4_v<D>(static_cast<const uint8_t *>(a.v_pages) + tile, slot % kFp4Tile, c,
-                      a.v_scale ? __ldg(a.v_scale + j) : 1.f, x);
-        store_bf16x16(vo, x);
+        place[threadIdx.x] = at;
+    }
+    __syncthreads();
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % G;
+    const int tasks = rows / kGroup * a.Hk;
+#pragma unroll 1
+    for (int task = warp; task < tasks; task += kThreads / 32) {
+        const int grp = task / a.Hk, j = task - grp * a.Hk;
+        const int row = grp * kGroup + lane / G;
+        const float gk = KIND == GQA_KV_FP4 && a.k_scale ? __ldg(a.k_scale + j) : 1.f;
+        const float gv = KIND == GQA_KV_FP4 && a.v_scale ? __ldg(a.v_scale + j) : 1.f;
+        Raw<KIND> k[kIts], v[kIts];
+        int q[kIts];
+#pragma unroll
+        for (int i = 0; i < kIts; ++i) {
+            const int at = place[row + i * kAt];
+            q[i] = at < 0 ? -1 : at + (j << pshift);
+            if (at < 0) continue;
+            fetch<KIND, D, false>(k[i], a.k_pages, a.k_scale, q[i], c, pshift);
+            fetch<KIND, D, true>(v[i], a.v_pages, a.v_scale, q[i], c, pshift);
+        }
+#pragma unroll
+        for (int i = 0; i < kIts; ++i) {
+            if (q[i] < 0) continue;
+            const long long r = r0 + row + i * kAt;
+            const size_t dst = (size_t)(a.paged ? (((r >> pshift) * a.Hk + j) << pshift) + (r & (P - 1)) : r * a.Hk + j) * D + c * 16;
+            uint32_t w[8];
+            convert<KIND, false>(k[i], q[i], gk, w);
+            store32(static_cast<uint16_t *>(a.k_out) + dst, w, wide);
+            convert<KIND, true>(v[i], q[i], gv, w);
+            store32(static_cast<uint16_t *>(a.v_out) + dst, w, wide);
+        }
     }
 }
 
@@ -140,16 +194,28 @@ __global__ void __launch_bounds__(256) read_kv_kernel(const ReadArgs a) {
 
 cudaError_t launch_read_kv(const ReadArgs &a, cudaStream_t stream) {
     if (a.B == 0 || a.total == 0) return cudaSuccess;
-    const long long rows = a.paged ? a.total * a.P : a.total;
-    const long long blocks = (rows * a.Hk * (a.D / 16) + 255) / 256;
+    // enough groups of 16 rows for a warp each, over the kv heads
+    const int rows = kGroup * (a.Hk >= 8 ? 1 : (8 + a.Hk - 1) / a.Hk);
+    const int pshift = a.P == 16 ? 4 : (a.P == 32 ? 5 : 6);
+    const long long total_rows = a.paged ? a.total << pshift : a.total;
+    const long long blocks = (total_rows + rows - 1) / rows;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    void (*k)(const ReadArgs);
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.k_out) | reinterpret_cast<uintptr_t>(a.v_out)) & 31) == 0;
+    void (*k)(const ReadArgs, int, long long, int, bool);
     if (a.kv_dtype == GQA_KV_FP4) k = a.D == 128 ? read_kv_kernel<GQA_KV_FP4, 128> : read_kv_kernel<GQA_KV_FP4, 64>;
     else if (a.kv_dtype == GQA_KV_FP8_E4M3)
         k = a.D == 128 ? read_kv_kernel<GQA_KV_FP8_E4M3, 128> : read_kv_kernel<GQA_KV_FP8_E4M3, 64>;
     else k = a.D == 128 ? read_kv_kernel<GQA_KV_BF16, 128> : read_kv_kernel<GQA_KV_BF16, 64>;
-    k<<<(unsigned)blocks, 256, 0, stream>>>(a);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, a, rows, total_rows, pshift, wide);
 }
 
 }  // namespace gqa

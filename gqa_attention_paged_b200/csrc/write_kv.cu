@@ -1,226 +1,309 @@
 // write_kv.cu -- writes the newest tokens of every sequence into the paged cache: a prefill
 // chunk's, or a decode step's one token ("TensorRT对Grouped Query Attention的支持进展", sections
 // "动态形状与KV Cache管理" and "与动态批处理协同"), quantised on the way for 4-bit and e4m3 pools.
+// Bound by HBM (16 bits in, 4 to 16 out).  The grid runs over the rows of the input, so that no CTA
+// is idle however ragged the chunks are; a thread per row first finds where the row goes.
 //
 // 4-bit pools (write_fp4_kernel).  A block of 16 dims of one token, with g the head's factor:
 //   a = max |x|,  sf = e4m3(min(fl(a / fl(6 g)), 448)),  s = fl(sf g),  code = e2m1(fl(x / s))
-// (fl: fp32 rounding).  The quotients are IEEE divisions: a reciprocal would move values off
-// the exact ties that bf16 inputs hit.  A block whose scale rounds to 0 stores zeros, one that
-// holds a NaN stores a NaN scale (it reads back as NaN), infinities saturate.  One thread per
-// (row, kv head, block): 32 bytes in, 8 code bytes and a scale byte out for K.  V bytes hold
-// two tokens, so the thread of the even token takes both (a chunk's first token may be the odd
-// one alone; half-written bytes keep their other nibble).
+// (fl: fp32 rounding).  The quotients are rounded as a division's: a reciprocal alone would move
+// values off the exact ties that bf16 inputs hit.  A block whose scale rounds to 0 stores zeros, one
+// that holds a NaN stores a NaN scale (it reads back as NaN), infinities saturate.  A V byte holds
+// two tokens, so a thread takes the blocks of a pair of tokens, of keys or of values (a chunk may
+// begin or end inside a pair; half-written bytes keep their other nibble).
 //
-// e4m3 and bf16 pools (write_page_kernel).  One CTA per (page of the chunk, kv head,
-// sequence).  A page whose first slot is in the chunk takes its scale from the chunk's tokens
-// in it, absmax / 448 (1 when they are all zero); a page that was begun earlier keeps its
-// scale.  A chunk of one token is gqa_paged_append_kv()'s rule.
+// e4m3 and bf16 pools (write_page_kernel).  Work is (page of a chunk, kv head, K or V): a team of a
+// warp per 16 slots holds its tokens in registers, so the input is read once.  A page whose first
+// slot is in the chunk takes its scale from the chunk's tokens in it, absmax / 448 (1 when they are
+// all zero); a page that was begun earlier keeps its scale.  A chunk of one token is
+// gqa_paged_append_kv()'s rule.
 #include "fp4.cuh"
 #include "quant_kv.h"
 
 namespace gqa {
 namespace {
 
-// Where sequence b's rows go: first row, number of rows, first token.  False (and the error
-// word set) when the lengths do not fit one another.
-__device__ __forceinline__ bool chunk_of(const WriteArgs &a, int b, int &row0, int &n, int &tok0) {
-    const int L = __ldg(a.seq_lens + b);
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxRows = 128;  // input rows of a CTA
+
+// A row of the input: its sequence's first row, number of rows and first token, and the row's own
+// token; `page` < 0: not written (the error word says so unless the row is of no sequence).
+struct Row {
+    int row0, n, t, page;
+};
+
+__device__ __forceinline__ Row find_row(const WriteArgs &a, const Sequences<int32_t> &seqs, long long r) {
+    Row x = {0, 0, 0, -1};
+    if (r >= a.total_q) return x;
+    const int b = a.cu_q ? sequence_of(seqs.cu, a.B, r) : (int)r, L = seqs.lens[b];
     if (a.cu_q) {
-        row0 = __ldg(a.cu_q + b);
-        n = __ldg(a.cu_q + b + 1) - row0;
+        x.row0 = seqs.cu[b];
+        x.n = seqs.cu[b + 1] - x.row0;
     } else {
-        row0 = b;
-        n = L > 0 ? 1 : 0;
+        x.row0 = b;
+        x.n = L > 0 ? 1 : 0;
     }
-    tok0 = L - n;
-    if (n < 0 || n > a.max_q_len || row0 < 0 || (long long)row0 + n > a.total_q || tok0 < 0 ||
+    const int tok0 = L - x.n;
+    if (x.n < 0 || x.n > a.max_q_len || x.row0 < 0 || (long long)x.row0 + x.n > a.total_q || tok0 < 0 ||
         L > a.pt_stride * a.P) {
         set_error(a.err, GQA_ERR_BAD_PAGE);
-        return false;
+        return x;
     }
-    return true;
+    if (r < x.row0 || r >= x.row0 + x.n) return x;
+    x.t = tok0 + (int)(r - x.row0);
+    const int phys = __ldg(a.page_table + (size_t)b * a.pt_stride + x.t / a.P);
+    if (phys < 0 || phys >= a.num_pages) set_error(a.err, GQA_ERR_BAD_PAGE);
+    else x.page = phys;
+    return x;
+}
+
+// Sequences none of whose rows are looked at (negative counts, rows past total_q) and that do not
+// fit are recorded here, each by one thread of the grid's x.
+__device__ __forceinline__ void check_sequences(const WriteArgs &a) {
+    if (!a.cu_q) return;
+    for (long long b = (long long)blockIdx.x * kThreads + threadIdx.x; b < a.B; b += (long long)gridDim.x * kThreads) {
+        const int L = __ldg(a.seq_lens + b), row0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - row0;
+        if (n < 0 || n > a.max_q_len || row0 < 0 || (long long)row0 + n > a.total_q || n > L || L > a.pt_stride * a.P)
+            set_error(a.err, GQA_ERR_BAD_PAGE);
+    }
+}
+
+__device__ __forceinline__ void load_block(const void *rows, long long stride, long long r, int at, float (&x)[16]) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(rows) + r * stride + at);
+    const uint4 lo = __ldg(p), hi = __ldg(p + 1);
+    unpack_bf16x8(lo, x);
+    unpack_bf16x8(hi, x + 8);
 }
 
 // Scale code of a block of 16 and its values over the scale; zeros where the scale is 0 or NaN.
-__device__ __forceinline__ uint32_t quantise_block(float (&x)[16], float g) {
+// `over6` divides by 6 g.
+__device__ __forceinline__ uint32_t quantise_block(float (&x)[16], float g, const Quotient &over6) {
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) a = max_nan(a, fabsf(x[i]));
-    const uint32_t sf = f32_to_e4m3(a / (6.f * g));
-    const float s = e4m3_to_f32(sf) * g;
+    const uint32_t sf = f32_to_e4m3(over6.fits(a) ? over6(a) : divide(a, over6.s));
+    const Quotient over(e4m3_to_f32(sf) * g);
+    if (over.fits(a)) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = s > 0.f ? x[i] / s : 0.f;
+        for (int i = 0; i < 16; ++i) x[i] = over(x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = over.s > 0.f ? divide(x[i], over.s) : 0.f;
+    }
     return sf;
 }
 
-__device__ __forceinline__ void load_block(const void *rows, long long stride, long long r, int at,
-                                           float (&x)[16]) {
-    const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(rows) + r * stride + at);
-    unpack_bf16x8(__ldg(p), x);
-    unpack_bf16x8(__ldg(p + 1), x + 8);
-}
-
 template <int D>
-__global__ void __launch_bounds__(256) write_fp4_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kThreads) write_fp4_kernel(const WriteArgs a, const int rows) {
     constexpr int G = D / 16, C = D / 8;
+    struct Pair {
+        int row, place, kind;  // first row, its pool row of head 0; 0: both tokens, 1: the even one, 2: the odd one
+    };
+    __shared__ Sequences<int32_t> seqs;
+    __shared__ Pair list[kMaxRows];
+    __shared__ int pairs;
+    const long long r0 = (long long)blockIdx.x * rows;
+    if (threadIdx.x == 0) pairs = 0;
     grid_dependency_wait();
     grid_dependents_launch();
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const int c = (int)(i % G), j = (int)(i / G % a.Hk);
-    const long long r = i / G / a.Hk;
-    if (r >= a.total_q) return;
-    const int b = a.cu_q ? sequence_of(a.cu_q, a.B, r) : (int)r;
-    int row0, n, tok0;
-    if (!chunk_of(a, b, row0, n, tok0) || r < row0 || r >= row0 + n) return;
-    const int t = tok0 + (int)(r - row0);
-    const int phys = __ldg(a.page_table + (size_t)b * a.pt_stride + t / a.P);
-    if (phys < 0 || phys >= a.num_pages) {
-        set_error(a.err, GQA_ERR_BAD_PAGE);
-        return;
-    }
-    const size_t tile = fp4_tile_offset(phys, a.Hk, j, a.P, t % a.P, D);
-    const int tok = t % kFp4Tile, pair = tok / 2;
-    const int at = j * D + c * 16;
-
-    // ---- K: this token's block
-    float x[16];
-    load_block(a.k_new, a.k_stride, r, at, x);
-    const uint32_t ks = quantise_block(x, a.k_scale ? __ldg(a.k_scale + j) : 1.f);
-    {
-        uint8_t *kt = static_cast<uint8_t *>(a.k_pages) + tile;
-        const float l0[4] = {x[0], x[2], x[4], x[6]}, h0[4] = {x[1], x[3], x[5], x[7]};
-        const float l1[4] = {x[8], x[10], x[12], x[14]}, h1[4] = {x[9], x[11], x[13], x[15]};
-        *reinterpret_cast<uint2 *>(kt + tok * (D / 2) + c * 8) =
-            make_uint2(f32_to_e2m1x8(l0, h0), f32_to_e2m1x8(l1, h1));
-        kt[8 * D + tok * G + c] = (uint8_t)ks;
-    }
-
-    // ---- V: the pair's blocks, by the even token's thread (or the odd one's, when it is the
-    // chunk's first)
-    const bool odd = tok & 1;
-    if (odd && r != row0) return;
-    const bool both = !odd && r + 1 < row0 + n;
-    const float gv = a.v_scale ? __ldg(a.v_scale + j) : 1.f;
-    float y[16];
-    uint32_t s0, s1 = 0;
-    load_block(a.v_new, a.v_stride, r, at, x);
-    s0 = quantise_block(x, gv);
-    if (both) {
-        load_block(a.v_new, a.v_stride, r + 1, at, y);
-        s1 = quantise_block(y, gv);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = 0.f;
-    }
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float l[4] = {x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]};
-        const float h[4] = {y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]};
-        w[e] = f32_to_e2m1x8(l, h);
-    }
-    uint8_t *vt = static_cast<uint8_t *>(a.v_pages) + tile;
-    uint8_t *sc = vt + 8 * D + pair * (2 * G) + c * 2;
-    uint8_t *codes = vt + (pair >> 2) * (4 * D) + (pair & 3) * C;
-    if (both) {
-        *reinterpret_cast<uint16_t *>(sc) = (uint16_t)(s0 | (s1 << 8));
-    } else {
-        sc[tok & 1] = (uint8_t)s0;
-        const uint32_t keep = odd ? 0x0f0f0f0fu : 0xf0f0f0f0u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int d = c * 16 + 4 * e;
-            const uint32_t old = *reinterpret_cast<const uint32_t *>(codes + (d / C) * (4 * C) + d % C);
-            w[e] = (old & keep) | ((odd ? w[e] << 4 : w[e]) & ~keep);
+    seqs.load(a.cu_q, a.seq_lens, a.B);
+    __syncthreads();
+    check_sequences(a);
+    if (threadIdx.x < rows) {
+        const long long r = r0 + threadIdx.x;
+        const Row x = find_row(a, seqs, r);
+        // a pair is its even token's, or the odd one's when that is the chunk's first
+        if (x.page >= 0) {
+            const bool odd = x.t & 1, both = !odd && r + 1 < x.row0 + x.n;
+            if (!odd || r == x.row0)
+                list[atomicAdd(&pairs, 1)] = {(int)r, x.page * a.Hk * a.P + x.t % a.P, both ? 0 : odd ? 2 : 1};
         }
     }
-    if constexpr (C == 16) {
-        *reinterpret_cast<uint4 *>(codes + c * (4 * C)) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-        *reinterpret_cast<uint2 *>(codes + (2 * c) * (4 * C)) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2 *>(codes + (2 * c + 1) * (4 * C)) = make_uint2(w[2], w[3]);
+    __syncthreads();
+
+    // ---- the threads run over blocks, then pairs, then heads, then K and V
+    const int np = pairs, units = np * G * a.Hk;
+#pragma unroll 1
+    for (int u = threadIdx.x; u < 2 * units; u += kThreads) {
+        const bool is_v = u >= units;
+        const int i = (is_v ? u - units : u) / G, c = u % G, j = i / np;
+        const Pair e = list[i - j * np];
+        const int q = e.place + j * a.P, tok = q % kFp4Tile;
+        const void *src = is_v ? a.v_new : a.k_new;
+        const long long stride = is_v ? a.v_stride : a.k_stride;
+        const float *factor = is_v ? a.v_scale : a.k_scale;
+        float x[16], y[16];
+        load_block(src, stride, e.row, j * D + c * 16, x);
+        load_block(src, stride, e.row + (e.kind == 0), j * D + c * 16, y);
+        const float g = factor ? __ldg(factor + j) : 1.f;
+        const Quotient over6(6.f * g);
+        const uint32_t s0 = quantise_block(x, g, over6), s1 = quantise_block(y, g, over6);
+        uint8_t *tile = static_cast<uint8_t *>(is_v ? a.v_pages : a.k_pages) + (size_t)(q / kFp4Tile) * fp4_tile_bytes(D);
+        if (!is_v) {
+            uint8_t *codes = tile + tok * (D / 2) + c * 8, *sc = tile + 8 * D + tok * G + c;
+            const float l0[4] = {x[0], x[2], x[4], x[6]}, h0[4] = {x[1], x[3], x[5], x[7]};
+            const float l1[4] = {x[8], x[10], x[12], x[14]}, h1[4] = {x[9], x[11], x[13], x[15]};
+            *reinterpret_cast<uint2 *>(codes) = make_uint2(f32_to_e2m1x8(l0, h0), f32_to_e2m1x8(l1, h1));
+            *sc = (uint8_t)s0;
+            if (e.kind != 0) continue;
+            const float m0[4] = {y[0], y[2], y[4], y[6]}, n0[4] = {y[1], y[3], y[5], y[7]};
+            const float m1[4] = {y[8], y[10], y[12], y[14]}, n1[4] = {y[9], y[11], y[13], y[15]};
+            *reinterpret_cast<uint2 *>(codes + D / 2) = make_uint2(f32_to_e2m1x8(m0, n0), f32_to_e2m1x8(m1, n1));
+            sc[G] = (uint8_t)s1;
+            continue;
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float l[4] = {x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]};
+            const float h[4] = {y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]};
+            w[k] = f32_to_e2m1x8(l, h);  // alone, a token is in both nibbles
+        }
+        const int pair = tok / 2;
+        uint8_t *sc = tile + 8 * D + pair * (2 * G) + c * 2;
+        uint8_t *codes = tile + (pair >> 2) * (4 * D) + (pair & 3) * C;
+        if (e.kind == 0) {
+            *reinterpret_cast<uint16_t *>(sc) = (uint16_t)(s0 | (s1 << 8));
+        } else {
+            sc[e.kind == 2] = (uint8_t)s0;
+            const uint32_t keep = e.kind == 2 ? 0x0f0f0f0fu : 0xf0f0f0f0u;  // the other token's
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int d = c * 16 + 4 * k;
+                const uint32_t old = *reinterpret_cast<const uint32_t *>(codes + (d / C) * (4 * C) + d % C);
+                w[k] = (old & keep) | (w[k] & ~keep);
+            }
+        }
+        if constexpr (C == 16) {
+            *reinterpret_cast<uint4 *>(codes + c * (4 * C)) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            *reinterpret_cast<uint2 *>(codes + (2 * c) * (4 * C)) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2 *>(codes + (2 * c + 1) * (4 * C)) = make_uint2(w[2], w[3]);
+        }
     }
 }
 
-constexpr int kPageThreads = 256;
-constexpr int kPageMaxChunks = 64 * 128 / 8 / kPageThreads;  // 16-byte loads a thread holds
+// A lane's `count` eights of a page by division: read again, out of the way of the others.
+__device__ __noinline__ void divide_eights(const uint16_t *src, long long src_step, uint8_t *dst, int dst_step, int count, float s) {
+#pragma unroll 1
+    for (int i = 0; i < 8 * count; ++i) {
+        const float x = __uint_as_float((uint32_t)src[(i >> 3) * src_step + (i & 7)] << 16);
+        dst[(i >> 3) * dst_step + (i & 7)] = (uint8_t)f32_to_e4m3(x / s);
+    }
+}
 
-template <bool FP8>
-__device__ __forceinline__ void write_page(const WriteArgs &a, const void *rows, long long stride,
-                                           void *pages, float *scales, long long row, int ntok, int slot,
-                                           int phys, int j, float *red) {
-    const int per = a.D / 8, chunks = ntok * per;  // 8 elements each
-    uint4 w[kPageMaxChunks];
-    float m = 0.f;
+// One CTA per (run of `rows` input rows, kv head): the pages whose first row of the chunk is in the
+// run, K and V of each.  TEAM warps hold a page's 16 TEAM slots.
+template <bool FP8, int D, int TEAM>
+__global__ void __launch_bounds__(kThreads, 4) write_page_kernel(const WriteArgs a, const int rows) {
+    constexpr int P = 16 * TEAM, kPer = D / 8, kAt = 32 / kPer, kIts = 16 / kAt;  // rows of a warp at once
+    struct Page {
+        int row, ntok, slot, phys;
+    };
+    __shared__ Sequences<int32_t> seqs;
+    __shared__ Page list[64];
+    __shared__ int pages;
+    __shared__ float red[kWarps];
+    const long long r0 = (long long)blockIdx.x * rows;
+    const int j = blockIdx.y;
+    if (threadIdx.x == 0) pages = 0;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    // the run's lines set out for L2 while its pages are looked up
+    for (int i = threadIdx.x; i < rows * (D / 64) * 2; i += kThreads) {
+        const long long r = r0 + i / (D / 64 * 2);
+        if (r < a.total_q)
+            prefetch_l2(static_cast<const uint16_t *>(i & 1 ? a.v_new : a.k_new) + r * (i & 1 ? a.v_stride : a.k_stride) + j * D +
+                        (i >> 1) % (D / 64) * 64);
+    }
+    seqs.load(a.cu_q, a.seq_lens, a.B);
+    __syncthreads();
+    if (j == 0) check_sequences(a);
+    if (threadIdx.x < rows) {
+        const long long r = r0 + threadIdx.x;
+        const Row x = find_row(a, seqs, r);
+        if (x.page >= 0 && (x.t % P == 0 || r == x.row0)) {
+            const int left = (int)(x.row0 + x.n - r);
+            list[atomicAdd(&pages, 1)] = {(int)r, min(P - x.t % P, left), x.t % P, x.page};
+        }
+    }
+    __syncthreads();
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / TEAM, part = warp % TEAM;
+#pragma unroll 1
+    for (int task = team; task < 2 * pages; task += kWarps / TEAM) {
+        const Page pg = list[task >> 1];
+        const bool is_v = task & 1;
+        const uint16_t *src = static_cast<const uint16_t *>(is_v ? a.v_new : a.k_new) + (size_t)j * D + (lane % kPer) * 8;
+        const long long stride = is_v ? a.v_stride : a.k_stride;
+        const int t0 = part * 16 + lane / kPer;  // this lane's first token of the page's
+        uint4 w[kIts];
+        float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPageMaxChunks; ++i) {
-        const int e = i * kPageThreads + threadIdx.x;
-        if (e >= chunks) continue;
-        w[i] = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const uint16_t *>(rows) +
-                                                     (row + e / per) * stride + (size_t)j * a.D + (e % per) * 8));
+        for (int i = 0; i < kIts; ++i)
+            w[i] = t0 + i * kAt < pg.ntok ? __ldg(reinterpret_cast<const uint4 *>(src + (pg.row + t0 + i * kAt) * stride))
+                                          : make_uint4(0u, 0u, 0u, 0u);
+        const size_t block = (size_t)pg.phys * a.Hk + j;
+        float s = 1.f;
         if (FP8) {
-            float x[8];
-            unpack_bf16x8(w[i], x);
+            float *scales = is_v ? a.v_scale : a.k_scale;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[k]));
+            for (int i = 0; i < kIts; ++i) {
+                float x[8];
+                unpack_bf16x8(w[i], x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[k]));
+            }
+            if (pg.slot == 0) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (TEAM > 1) {
+                    if (lane == 0) red[warp] = m;
+                    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * TEAM) : "memory");
+#pragma unroll
+                    for (int k = 0; k < TEAM; ++k) m = fmaxf(m, red[team * TEAM + k]);
+                    // (the next page of the team is written after all have read this one's)
+                    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * TEAM) : "memory");
+                }
+                s = m > 0.f ? m / 448.f : 1.f;
+                if (part == 0 && lane == 0) scales[block] = s;
+            } else {
+                s = scales[block];
+            }
         }
-    }
-    const size_t block = (size_t)phys * a.Hk + j;
-    float s = 1.f;
-    if (FP8) {
-        if (slot == 0) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-            __syncthreads();
-            m = 0.f;
-            for (int k = 0; k < kPageThreads / 32; ++k) m = fmaxf(m, red[k]);
-            s = m > 0.f ? m / 448.f : 1.f;
-            if (threadIdx.x == 0) scales[block] = s;
-        } else {
-            s = scales[block];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kPageMaxChunks; ++i) {
-        const int e = i * kPageThreads + threadIdx.x;
-        if (e >= chunks) continue;
-        const size_t at = (block * a.P + slot + e / per) * a.D + (e % per) * 8;
+        const size_t at = (block * P + pg.slot + t0) * D + (lane % kPer) * 8;
+        void *dst = is_v ? a.v_pages : a.k_pages;
         if (!FP8) {
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(pages) + at) = w[i];
-        } else {
+#pragma unroll
+            for (int i = 0; i < kIts; ++i)
+                if (t0 + i * kAt < pg.ntok) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst) + at + i * kAt * D) = w[i];
+            continue;
+        }
+        const Quotient over(s);
+        if (!over.fits(m)) {
+            const int count = min(kIts, (pg.ntok - t0 + kAt - 1) / kAt);
+            divide_eights(src + (pg.row + t0) * stride, kAt * stride, static_cast<uint8_t *>(dst) + at, kAt * D, count, s);
+            continue;
+        }
+#pragma unroll
+        for (int i = 0; i < kIts; ++i) {
+            if (t0 + i * kAt >= pg.ntok) continue;
             float x[8];
             unpack_bf16x8(w[i], x);
-            uint32_t c[2] = {0u, 0u};
+            uint32_t c[2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                c[k / 4] |= (uint32_t)__nv_cvt_float_to_fp8(x[k] / s, __NV_SATFINITE, __NV_E4M3) << (8 * (k % 4));
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pages) + at) = make_uint2(c[0], c[1]);
+            for (int k = 0; k < 2; ++k)
+                c[k] = f32_to_e4m3x2(over(x[4 * k]), over(x[4 * k + 1])) |
+                       f32_to_e4m3x2(over(x[4 * k + 2]), over(x[4 * k + 3])) << 16;
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(dst) + at + i * kAt * D) = make_uint2(c[0], c[1]);
         }
     }
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(kPageThreads) write_page_kernel(const WriteArgs a) {
-    __shared__ float red[2][kPageThreads / 32];
-    const int j = blockIdx.y, b = blockIdx.z;
-    grid_dependency_wait();
-    grid_dependents_launch();
-    int row0, n, tok0;
-    if (!chunk_of(a, b, row0, n, tok0) || n == 0) return;  // uniform for the CTA
-    const long long page = (long long)tok0 / a.P + blockIdx.x;
-    const long long t0 = blockIdx.x == 0 ? tok0 : page * a.P;
-    const long long t1 = min((page + 1) * a.P, (long long)tok0 + n);
-    if (t0 >= t1) return;
-    const int phys = __ldg(a.page_table + (size_t)b * a.pt_stride + page);
-    if (phys < 0 || phys >= a.num_pages) {
-        if (threadIdx.x == 0) set_error(a.err, GQA_ERR_BAD_PAGE);
-        return;
-    }
-    const long long row = row0 + (t0 - tok0);
-    const int slot = (int)(t0 - page * a.P), ntok = (int)(t1 - t0);
-    write_page<FP8>(a, a.k_new, a.k_stride, a.k_pages, a.k_scale, row, ntok, slot, phys, j, red[0]);
-    write_page<FP8>(a, a.v_new, a.v_stride, a.v_pages, a.v_scale, row, ntok, slot, phys, j, red[1]);
+template <bool FP8, int D>
+void (*page_kernel(int P))(const WriteArgs, int) {
+    return P == 16 ? write_page_kernel<FP8, D, 1> : P == 32 ? write_page_kernel<FP8, D, 2> : write_page_kernel<FP8, D, 4>;
 }
 
 }  // namespace
@@ -231,22 +314,28 @@ cudaError_t launch_write_kv(const WriteArgs &a, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    void (*k)(const WriteArgs, int);
+    int rows;
     if (a.kv_dtype == GQA_KV_FP4) {
-        const long long blocks = ((long long)a.total_q * a.Hk * (a.D / 16) + 255) / 256;
-        if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-        cfg.gridDim = dim3((unsigned)blocks);
-        cfg.blockDim = dim3(256);
-        return a.D == 128 ? cudaLaunchKernelEx(&cfg, write_fp4_kernel<128>, a)
-                          : cudaLaunchKernelEx(&cfg, write_fp4_kernel<64>, a);
+        // as few rows as give every thread a block, more once that fills the GPU several times
+        rows = 2;
+        while (rows < kMaxRows && rows * a.Hk * (a.D / 16) < kThreads) rows *= 2;
+        while (rows < 32 && a.total_q / rows > 592) rows *= 2;
+        cfg.gridDim = dim3((unsigned)(((long long)a.total_q + rows - 1) / rows));
+        k = a.D == 128 ? write_fp4_kernel<128> : write_fp4_kernel<64>;
+    } else {
+        // chunks of some length: a page or a few per CTA; single tokens are a page each, which a CTA
+        // takes 8 / TEAM at a time
+        rows = a.total_q >= 16LL * a.B ? 64 : 8;
+        cfg.gridDim = dim3((unsigned)(((long long)a.total_q + rows - 1) / rows), a.Hk);
+        if (a.kv_dtype == GQA_KV_FP8_E4M3) k = a.D == 128 ? page_kernel<true, 128>(a.P) : page_kernel<true, 64>(a.P);
+        else k = a.D == 128 ? page_kernel<false, 128>(a.P) : page_kernel<false, 64>(a.P);
     }
-    // pages that max_q_len tokens can touch, wherever they begin
-    cfg.gridDim = dim3((unsigned)(((long long)a.max_q_len + a.P - 2) / a.P + 1), a.Hk, a.B);
-    cfg.blockDim = dim3(kPageThreads);
-    return a.kv_dtype == GQA_KV_FP8_E4M3 ? cudaLaunchKernelEx(&cfg, write_page_kernel<true>, a)
-                                         : cudaLaunchKernelEx(&cfg, write_page_kernel<false>, a);
+    return cudaLaunchKernelEx(&cfg, k, a, rows);
 }
 
 }  // namespace gqa
