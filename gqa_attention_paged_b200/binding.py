@@ -122,7 +122,11 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
+def _need(t: torch.Tensor, name: str, dtype=None, shape=None, here=None):
+    """A contiguous CUDA tensor of this dtype and shape, on device `here` if one is given."""
+    if (here is not None and isinstance(t, torch.Tensor) and t.get_device() == here
+            and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -134,19 +138,22 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if here is not None and t.get_device() != here:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{here}")
 
 
-def _need_here(*tensors):
-    """All of them (None apart) on the current device, whose stream the call uses."""
+def _device_of(k_pages: torch.Tensor) -> int:
+    """The device of a call on these pools, which has to be the current one."""
+    _need(k_pages, "k_pages", _KV_DTYPES)
     here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"a tensor is on cuda:{t.get_device()}, the current device is cuda:{here}")
+    if k_pages.get_device() != here:
+        raise ValueError(f"k_pages is on cuda:{k_pages.get_device()}, the current device is cuda:{here}")
+    return here
 
 
-def _need_word(workspace: torch.Tensor):
+def _need_word(here: int, workspace: torch.Tensor):
     """A workspace with room for the error word."""
-    _need(workspace, "workspace", torch.uint8)
+    _need(workspace, "workspace", torch.uint8, None, here)
     if workspace.numel() < 256:
         raise ValueError("workspace must have 256 bytes at least")
 
@@ -171,18 +178,22 @@ def _kv_layout(t: torch.Tensor) -> Tuple[int, int]:
     return GQA_KV_FP8_E4M3, row
 
 
-def _need_scales(kv_dtype: int, num_pages: int, Hk: int, k_scale, v_scale):
+def _need_scales(kv_dtype: int, num_pages: int, Hk: int, k_scale, v_scale, here=None):
     """e4m3 pools need scales [num_pages][Hk]; 4-bit pools take factors [Hk] or None."""
-    if kv_dtype == GQA_KV_FP8_E4M3:
-        if k_scale is None or v_scale is None:
-            raise ValueError("fp8 KV needs k_scale and v_scale")
-        _need(k_scale, "k_scale", torch.float32, (num_pages, Hk))
-        _need(v_scale, "v_scale", torch.float32, (num_pages, Hk))
-    elif kv_dtype == GQA_KV_FP4:
-        if k_scale is not None:
-            _need(k_scale, "k_scale", torch.float32, (Hk,))
-        if v_scale is not None:
-            _need(v_scale, "v_scale", torch.float32, (Hk,))
+    if kv_dtype == GQA_KV_BF16:
+        return
+    if kv_dtype == GQA_KV_FP8_E4M3 and (k_scale is None or v_scale is None):
+        raise ValueError("fp8 KV needs k_scale and v_scale")
+    shape = (num_pages, Hk) if kv_dtype == GQA_KV_FP8_E4M3 else (Hk,)
+    if k_scale is not None:
+        _need(k_scale, "k_scale", torch.float32, shape, here)
+    if v_scale is not None:
+        _need(v_scale, "v_scale", torch.float32, shape, here)
+
+
+def _four_bit_device(kv_dtype: int, k_pages: torch.Tensor) -> Optional[int]:
+    """Calls on 4-bit pools take tensors of the current device alone; None for other pools."""
+    return _device_of(k_pages) if kv_dtype == GQA_KV_FP4 else None
 
 
 # ------------------------------------------------------------------------ raw ABI names
@@ -225,33 +236,32 @@ def gqa_paged_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     (uint8/float8_e4m3fn with fp32 scales [num_pages][Hk]), or 4-bit (new_fp4_pool; optional
     fp32 factors [Hk] as k_scale / v_scale); page_table int32 [B][pt_stride];
     seq_lens int32 [B].  Returns (out bf16 [B][Hq][D], lse fp32 [B][Hq] or None)."""
-    _need(q, "q", torch.bfloat16)
-    B, Hq, D = q.shape
     _need(k_pages, "k_pages", _KV_DTYPES)
-    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
     kv_dtype, D2 = _kv_layout(k_pages)
+    here = _four_bit_device(kv_dtype, k_pages)
+    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape, here)
+    _need(q, "q", torch.bfloat16, None, here)
+    B, Hq, D = q.shape
     num_pages, Hk, P, _ = k_pages.shape
     if D2 != D:
         raise ValueError("head_dim of q and the KV pools differ")
-    _need(page_table, "page_table", torch.int32)
-    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    _need(page_table, "page_table", torch.int32, None, here)
+    _need(seq_lens, "seq_lens", torch.int32, (B,), here)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B][pt_stride]")
-    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
+    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale, here)
     pt_stride = page_table.shape[1]
     if out is None:
         out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", torch.bfloat16, (B, Hq, D))
+    _need(out, "out", torch.bfloat16, (B, Hq, D), here)
     if lse is None and want_lse:
         lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
     if lse is not None:
-        _need(lse, "lse", torch.float32, (B, Hq))
+        _need(lse, "lse", torch.float32, (B, Hq), here)
     if workspace is None:  # (a given one's size is checked by the call)
         workspace = new_workspace(gqa_paged_decode_workspace_size(
             B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits), q.device)
-    _need(workspace, "workspace", torch.uint8)
-    if kv_dtype == GQA_KV_FP4:
-        _need_here(q, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, out, lse, workspace)
+    _need(workspace, "workspace", torch.uint8, None, here)
     st = load().gqa_paged_decode(
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), kv_dtype,
         _ptr(page_table), pt_stride, _ptr(seq_lens), B, Hq, Hk, D, P, num_pages, float(scale),
@@ -273,33 +283,31 @@ def gqa_paged_decode_partial(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
     """Decode over the tokens page_table / seq_lens cover, as one split's fp32 partial
     result: (o_part fp32 [B][Hq][D] normalised, lse_part fp32 [B][Hq]), the inputs
     lse_combine merges."""
-    _need(q, "q", torch.bfloat16)
-    B, Hq, D = q.shape
     _need(k_pages, "k_pages", _KV_DTYPES)
-    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
     kv_dtype, D2 = _kv_layout(k_pages)
+    here = _four_bit_device(kv_dtype, k_pages)
+    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape, here)
+    _need(q, "q", torch.bfloat16, None, here)
+    B, Hq, D = q.shape
     num_pages, Hk, P, _ = k_pages.shape
     if D2 != D:
         raise ValueError("head_dim of q and the KV pools differ")
-    _need(page_table, "page_table", torch.int32)
-    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    _need(page_table, "page_table", torch.int32, None, here)
+    _need(seq_lens, "seq_lens", torch.int32, (B,), here)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B][pt_stride]")
-    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
+    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale, here)
     pt_stride = page_table.shape[1]
     if o_part is None:
         o_part = torch.empty(B, Hq, D, dtype=torch.float32, device=q.device)
-    _need(o_part, "o_part", torch.float32, (B, Hq, D))
+    _need(o_part, "o_part", torch.float32, (B, Hq, D), here)
     if lse_part is None:
         lse_part = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
-    _need(lse_part, "lse_part", torch.float32, (B, Hq))
+    _need(lse_part, "lse_part", torch.float32, (B, Hq), here)
     if workspace is None:  # (a given one's size is checked by the call)
         workspace = new_workspace(gqa_paged_decode_workspace_size(
             B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits), q.device)
-    _need(workspace, "workspace", torch.uint8)
-    if kv_dtype == GQA_KV_FP4:
-        _need_here(q, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, o_part, lse_part,
-                   workspace)
+    _need(workspace, "workspace", torch.uint8, None, here)
     st = load().gqa_paged_decode_partial(
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), kv_dtype,
         _ptr(page_table), pt_stride, _ptr(seq_lens), B, Hq, Hk, D, P, num_pages, float(scale),
@@ -321,26 +329,25 @@ def gqa_paged_decode_static_scratch(q: torch.Tensor, k_pages: torch.Tensor,
     """gqa_paged_decode without a workspace: the library's fixed scratch array is used
     (for callers that cannot allocate device memory; see include/gqa_paged.h).  `out` and
     `lse` must be passed in by such callers; they are only created here for convenience."""
-    _need(q, "q", torch.bfloat16)
-    B, Hq, D = q.shape
     _need(k_pages, "k_pages", _KV_DTYPES)
-    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
     kv_dtype, D2 = _kv_layout(k_pages)
+    here = _four_bit_device(kv_dtype, k_pages)
+    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape, here)
+    _need(q, "q", torch.bfloat16, None, here)
+    B, Hq, D = q.shape
     num_pages, Hk, P, _ = k_pages.shape
     if D2 != D:
         raise ValueError("head_dim of q and the KV pools differ")
-    _need(page_table, "page_table", torch.int32)
-    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    _need(page_table, "page_table", torch.int32, None, here)
+    _need(seq_lens, "seq_lens", torch.int32, (B,), here)
     if kv_dtype == GQA_KV_FP4:
-        _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
+        _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale, here)
     if out is None:
         out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=q.device)
     if lse is None:
         lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
-    _need(out, "out", torch.bfloat16, (B, Hq, D))
-    _need(lse, "lse", torch.float32, (B, Hq))
-    if kv_dtype == GQA_KV_FP4:
-        _need_here(q, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, out, lse)
+    _need(out, "out", torch.bfloat16, (B, Hq, D), here)
+    _need(lse, "lse", torch.float32, (B, Hq), here)
     st = load().gqa_paged_decode_static_scratch(
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), kv_dtype,
         _ptr(page_table), page_table.shape[1], _ptr(seq_lens), B, Hq, Hk, D, P, num_pages,
@@ -352,20 +359,19 @@ def gqa_paged_decode_static_scratch(q: torch.Tensor, k_pages: torch.Tensor,
 
 def _append_args(k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale):
     _need(k_pages, "k_pages", _KV_DTYPES)
-    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
     kv_dtype, D = _kv_layout(k_pages)
+    here = _four_bit_device(kv_dtype, k_pages)
+    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape, here)
     num_pages, Hk, P, _ = k_pages.shape
-    _need(seq_lens, "seq_lens", torch.int32)
+    _need(seq_lens, "seq_lens", torch.int32, None, here)
     B = seq_lens.shape[0]
-    _need(k_new, "k_new", torch.bfloat16, (B, Hk, D))
-    _need(v_new, "v_new", torch.bfloat16, (B, Hk, D))
-    _need(page_table, "page_table", torch.int32)
+    _need(k_new, "k_new", torch.bfloat16, (B, Hk, D), here)
+    _need(v_new, "v_new", torch.bfloat16, (B, Hk, D), here)
+    _need(page_table, "page_table", torch.int32, None, here)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B][pt_stride]")
-    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
-    if kv_dtype == GQA_KV_FP4:
-        _need_here(k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale)
-    return B, Hk, D, P, num_pages, kv_dtype
+    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale, here)
+    return B, Hk, D, P, num_pages, kv_dtype, here
 
 
 def gqa_paged_append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
@@ -376,14 +382,13 @@ def gqa_paged_append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch
     """Write token seq_lens[b] - 1 of every sequence (k_new / v_new bf16 [B][Hk][D]) into
     the paged cache, in place (e4m3 and 4-bit pools quantise it; see include/gqa_paged.h).  Returns
     the workspace holding the error word."""
-    B, Hk, D, P, num_pages, kv_dtype = _append_args(k_new, v_new, k_pages, v_pages, page_table,
-                                                     seq_lens, k_scale, v_scale)
+    B, Hk, D, P, num_pages, kv_dtype, here = _append_args(
+        k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale)
     if workspace is None:
         workspace = new_workspace(256, k_pages.device)
-    _need(workspace, "workspace", torch.uint8)
     if kv_dtype == GQA_KV_FP4:
-        _need_word(workspace)
-        _need_here(workspace)
+        _need_word(here, workspace)
+    _need(workspace, "workspace", torch.uint8)
     st = load().gqa_paged_append_kv(
         _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
         kv_dtype, _ptr(page_table), page_table.shape[1], _ptr(seq_lens), B, Hk, D, P, num_pages,
@@ -402,26 +407,24 @@ def gqa_paged_append_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.T
                             workspace: Optional[torch.Tensor] = None, want_lse: bool = True,
                             stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """gqa_paged_append_kv then gqa_paged_decode on one stream."""
-    _need(q, "q", torch.bfloat16)
-    B, Hk, D, P, num_pages, kv_dtype = _append_args(k_new, v_new, k_pages, v_pages, page_table,
-                                                     seq_lens, k_scale, v_scale)
+    B, Hk, D, P, num_pages, kv_dtype, here = _append_args(
+        k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale)
+    _need(q, "q", torch.bfloat16, None, here)
     Bq, Hq, Dq = q.shape
     if Bq != B or Dq != D:
         raise ValueError("q must be [B][Hq][head_dim] with the pools' head_dim")
     pt_stride = page_table.shape[1]
     if out is None:
         out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", torch.bfloat16, (B, Hq, D))
+    _need(out, "out", torch.bfloat16, (B, Hq, D), here)
     if lse is None and want_lse:
         lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
     if lse is not None:
-        _need(lse, "lse", torch.float32, (B, Hq))
+        _need(lse, "lse", torch.float32, (B, Hq), here)
     if workspace is None:  # (a given one's size is checked by the call)
         workspace = new_workspace(gqa_paged_decode_workspace_size(
             B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits), q.device)
-    _need(workspace, "workspace", torch.uint8)
-    if kv_dtype == GQA_KV_FP4:
-        _need_here(q, out, lse, workspace)
+    _need(workspace, "workspace", torch.uint8, None, here)
     st = load().gqa_paged_append_decode(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
         _ptr(v_scale), kv_dtype, _ptr(page_table), pt_stride, _ptr(seq_lens), B, Hq, Hk, D, P,
@@ -495,20 +498,40 @@ def new_fp4_pool(num_pages: int, Hk: int, page_size: int, head_dim: int, device)
                        device=device)
 
 
-def _need_rows(t: torch.Tensor, name: str, shape):
-    """bf16 rows [T][Hk][D]: contiguous inside a row, any distance between rows."""
+def _need_rows(here: int, t: torch.Tensor, name: str, shape) -> int:
+    """bf16 rows [T][Hk][D]: contiguous inside a row, any distance between rows, which is returned."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
-    if t.dtype != torch.bfloat16:
+    if t.get_device() != here:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{here}")
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {torch.bfloat16}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     T, Hk, D = shape
-    if t.numel() and (t.stride(2) != 1 or (Hk > 1 and t.stride(1) != D)):
+    if t.is_contiguous():
+        return Hk * D
+    if t.stride(2) != 1 or (Hk > 1 and t.stride(1) != D):
         raise ValueError(f"{name}: the [Hk][head_dim] values of a row must be contiguous")
     return t.stride(0) if T > 1 else Hk * D
+
+
+def _pools_on(here: int, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale, v_scale):
+    """Checks of the value pool and the scales; (kv_dtype, head_dim, num_pages, Hk, page_size)."""
+    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape, here)
+    kv_dtype, D = _kv_layout(k_pages)
+    num_pages, Hk, P, _ = k_pages.shape
+    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale, here)
+    return kv_dtype, D, num_pages, Hk, P
+
+
+def _table_on(here: int, page_table: torch.Tensor, B: int) -> int:
+    _need(page_table, "page_table", torch.int32, None, here)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B][pt_stride]")
+    return page_table.shape[1]
 
 
 def gqa_paged_write_kv(k_new: torch.Tensor, v_new: torch.Tensor, cu_q: torch.Tensor,
@@ -521,28 +544,22 @@ def gqa_paged_write_kv(k_new: torch.Tensor, v_new: torch.Tensor, cu_q: torch.Ten
     [total_q][Hk][D], rows of any stride; cu_q int32 [B+1]) into the paged cache, in place;
     e4m3 and 4-bit pools quantise them (see include/gqa_paged.h).  Returns the workspace holding
     the error word."""
-    _need(k_pages, "k_pages", _KV_DTYPES)
-    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
-    kv_dtype, D = _kv_layout(k_pages)
-    num_pages, Hk, P, _ = k_pages.shape
-    _need(seq_lens, "seq_lens", torch.int32)
+    here = _device_of(k_pages)
+    kv_dtype, D, num_pages, Hk, P = _pools_on(here, k_pages, v_pages, k_scale, v_scale)
+    _need(seq_lens, "seq_lens", torch.int32, None, here)
     B, T = seq_lens.shape[0], k_new.shape[0]
-    ks = _need_rows(k_new, "k_new", (T, Hk, D))
-    vs = _need_rows(v_new, "v_new", (T, Hk, D))
-    _need(cu_q, "cu_q", torch.int32, (B + 1,))
-    _need(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be [B][pt_stride]")
-    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
+    ks = _need_rows(here, k_new, "k_new", (T, Hk, D))
+    vs = _need_rows(here, v_new, "v_new", (T, Hk, D))
+    _need(cu_q, "cu_q", torch.int32, (B + 1,), here)
+    pt_stride = _table_on(here, page_table, B)
     if workspace is None:
         workspace = new_workspace(256, k_pages.device)
-    _need_word(workspace)
-    _need_here(k_new, v_new, cu_q, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, workspace)
+    _need_word(here, workspace)
     if T == 0:
         return workspace
     st = load().gqa_paged_write_kv(
         _ptr(k_new), _ptr(v_new), ks, vs, _ptr(cu_q), _ptr(k_pages), _ptr(v_pages),
-        _ptr(k_scale), _ptr(v_scale), kv_dtype, _ptr(page_table), page_table.shape[1],
+        _ptr(k_scale), _ptr(v_scale), kv_dtype, _ptr(page_table), pt_stride,
         _ptr(seq_lens), B, Hk, D, P, num_pages, T, int(max_q_len), _ptr(workspace),
         _stream(stream))
     _check("gqa_paged_write_kv", st)
@@ -561,37 +578,30 @@ def gqa_paged_read_kv(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: 
     bf16, e4m3 or 4-bit pools: (k, v) [total][Hk][D] rows at cu_out (int64 [B+1]), or, with
     `paged`, bf16 pages [total][Hk][P][D] with cu_out counting pages (page cu_out[b] + i holds
     the i-th page of the stretch; slots outside it are not written)."""
-    _need(k_pages, "k_pages", _KV_DTYPES)
-    _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
-    kv_dtype, D = _kv_layout(k_pages)
-    num_pages, Hk, P, _ = k_pages.shape
-    _need(seq_lens, "seq_lens", torch.int32)
+    here = _device_of(k_pages)
+    kv_dtype, D, num_pages, Hk, P = _pools_on(here, k_pages, v_pages, k_scale, v_scale)
+    _need(seq_lens, "seq_lens", torch.int32, None, here)
     B = seq_lens.shape[0]
-    _need(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2 or page_table.shape[0] != B:
-        raise ValueError("page_table must be [B][pt_stride]")
-    _need(cu_out, "cu_out", torch.int64, (B + 1,))
+    pt_stride = _table_on(here, page_table, B)
+    _need(cu_out, "cu_out", torch.int64, (B + 1,), here)
     if starts is not None:
-        _need(starts, "starts", torch.int32, (B,))
-    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale)
+        _need(starts, "starts", torch.int32, (B,), here)
     total = int(total)
     shape = (total, Hk, P, D) if paged else (total, Hk, D)
     if k_out is None:
         k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
-    _need(k_out, "k_out", torch.bfloat16, shape)
-    _need(v_out, "v_out", torch.bfloat16, shape)
+    _need(k_out, "k_out", torch.bfloat16, shape, here)
+    _need(v_out, "v_out", torch.bfloat16, shape, here)
     if workspace is None:
         workspace = new_workspace(256, k_pages.device)
-    _need_word(workspace)
-    _need_here(k_pages, v_pages, page_table, seq_lens, cu_out, starts, k_scale, v_scale, k_out, v_out,
-               workspace)
+    _need_word(here, workspace)
     if total == 0:
         return k_out, v_out
     st = load().gqa_paged_read_kv(
         _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), kv_dtype, _ptr(page_table),
-        page_table.shape[1], _ptr(starts), _ptr(seq_lens), _ptr(cu_out), B, Hk, D, P, num_pages,
+        pt_stride, _ptr(starts), _ptr(seq_lens), _ptr(cu_out), B, Hk, D, P, num_pages,
         total, int(bool(paged)), _ptr(k_out), _ptr(v_out), _ptr(workspace), _stream(stream))
     _check("gqa_paged_read_kv", st)
     return k_out, v_out

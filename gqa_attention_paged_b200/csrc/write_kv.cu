@@ -95,7 +95,7 @@ __device__ __forceinline__ uint32_t quantise_block(float (&x)[16], float g, cons
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) write_fp4_kernel(const WriteArgs a, const int rows) {
+__global__ void __launch_bounds__(kThreads, 4) write_fp4_kernel(const WriteArgs a, const int rows) {
     constexpr int G = D / 16, C = D / 8;
     struct Pair {
         int row, place, kind;  // first row, its pool row of head 0; 0: both tokens, 1: the even one, 2: the odd one
@@ -109,7 +109,6 @@ __global__ void __launch_bounds__(kThreads) write_fp4_kernel(const WriteArgs a, 
     grid_dependents_launch();
     seqs.load(a.cu_q, a.seq_lens, a.B);
     __syncthreads();
-    check_sequences(a);
     if (threadIdx.x < rows) {
         const long long r = r0 + threadIdx.x;
         const Row x = find_row(a, seqs, r);
@@ -182,6 +181,7 @@ __global__ void __launch_bounds__(kThreads) write_fp4_kernel(const WriteArgs a, 
             *reinterpret_cast<uint2 *>(codes + (2 * c + 1) * (4 * C)) = make_uint2(w[2], w[3]);
         }
     }
+    check_sequences(a);
 }
 
 // A lane's `count` eights of a page by division: read again, out of the way of the others.
@@ -219,7 +219,6 @@ __global__ void __launch_bounds__(kThreads, 4) write_page_kernel(const WriteArgs
     }
     seqs.load(a.cu_q, a.seq_lens, a.B);
     __syncthreads();
-    if (j == 0) check_sequences(a);
     if (threadIdx.x < rows) {
         const long long r = r0 + threadIdx.x;
         const Row x = find_row(a, seqs, r);
@@ -299,6 +298,7 @@ __global__ void __launch_bounds__(kThreads, 4) write_page_kernel(const WriteArgs
             *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(dst) + at + i * kAt * D) = make_uint2(c[0], c[1]);
         }
     }
+    if (j == 0) check_sequences(a);
 }
 
 template <bool FP8, int D>

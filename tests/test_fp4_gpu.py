@@ -491,6 +491,60 @@ def test_decode_offsets_past_32_bits():
         assert np.array_equal(got.double().cpu().numpy(), np.concatenate([small.values(0, i), small.values(1, i)]))
 
 
+def test_calls_refuse_another_device(monkeypatch):
+    """The current stream belongs to the current device: tensors of another one are refused."""
+    c = Cache([20, 16], 1, 64, 16, seed=3).fill()
+    d, q = c.to_gpu(), queries(c, 2, 4).to(DEV)
+    k = torch.zeros(2, 1, 64, dtype=torch.bfloat16, device=DEV)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: binding.gqa_paged_decode(q, scale=0.1, **d),
+                 lambda: binding.gqa_paged_decode_partial(q, scale=0.1, **d),
+                 lambda: binding.gqa_paged_decode_static_scratch(q, scale=0.1, **d),
+                 lambda: binding.gqa_paged_append_kv(k, k, **d),
+                 lambda: binding.gqa_paged_append_decode(q, k, k, scale=0.1, **d),
+                 lambda: binding.gqa_paged_write_kv(k, k, cu_of([1, 1]), d["k_pages"], d["v_pages"], d["page_table"],
+                                                    d["seq_lens"], 1),
+                 lambda: binding.gqa_paged_read_kv(d["k_pages"], d["v_pages"], d["page_table"], d["seq_lens"],
+                                                   cu_of([20, 16], torch.int64), 36)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+
+
+def test_binding_refuses_what_does_not_fit():
+    c = Cache([20, 16], 2, 64, 16, seed=3).fill()
+    d, q = c.to_gpu(), queries(c, 2, 4).to(DEV)
+    k = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device=DEV)
+    cu, cu64 = cu_of([1, 1]), cu_of([20, 16], torch.int64)
+    pools = (d["k_pages"], d["v_pages"], d["page_table"], d["seq_lens"])
+    bad = torch.ones(3, device=DEV)
+    with pytest.raises(ValueError, match="k_scale"):
+        binding.gqa_paged_decode(q, *pools, 0.1, k_scale=bad)
+    with pytest.raises(ValueError, match="v_scale"):
+        binding.gqa_paged_write_kv(k, k, cu, *pools, 1, v_scale=bad)
+    with pytest.raises(ValueError, match="head_dim"):
+        binding.gqa_paged_decode(torch.zeros(2, 4, 128, dtype=torch.bfloat16, device=DEV), *pools, 0.1)
+    with pytest.raises(ValueError, match="contiguous"):
+        wide = torch.zeros(2, 2, 128, dtype=torch.bfloat16, device=DEV)
+        binding.gqa_paged_write_kv(wide[..., :64], k, cu, *pools, 1)
+    with pytest.raises(ValueError, match="shape"):
+        binding.gqa_paged_write_kv(k, k[:, :1], cu, *pools, 1)
+    with pytest.raises(TypeError):
+        binding.gqa_paged_write_kv(k.float(), k, cu, *pools, 1)
+    with pytest.raises(TypeError):
+        binding.gqa_paged_read_kv(*pools, cu, 36)
+    with pytest.raises(ValueError, match="shape"):
+        binding.gqa_paged_read_kv(*pools, cu64, 36, k_out=k, v_out=k)
+    with pytest.raises(ValueError, match="workspace"):
+        binding.gqa_paged_read_kv(*pools, cu64, 36, workspace=torch.zeros(64, dtype=torch.uint8, device=DEV))
+    with pytest.raises(binding.GQAError):
+        binding.gqa_paged_decode(q, *pools, 0.1, num_splits=2)
+    with pytest.raises(binding.GQAError):
+        binding.gqa_paged_decode(q, *pools, 0.1, workspace=torch.zeros(256, dtype=torch.uint8, device=DEV))
+    # rows of one token need no contiguous stride
+    one = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device=DEV)[::4]
+    binding.gqa_paged_write_kv(one, one, cu_of([1, 0]), *pools, 1)
+
+
 # ----------------------------------------------------------------------- streams, graphs, all together
 
 def test_decode_in_a_graph_and_on_another_stream():
