@@ -225,7 +225,7 @@ struct State {
         const uint4 *src = reinterpret_cast<const uint4 *>(rows + (size_t)(gq < n ? gq : 0) * D + cq * (D / 4));
         uint32_t w[D / 8], big = 0;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint4 *>(w + 4 * i) = __ldg(src + i);
+        for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint4 *>(w + 4 * i) = gq < n ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) big = __vmaxu2(big, w[i] & 0x7fff7fffu);
         big = __vmaxu2(big, __shfl_xor_sync(kFull, big, 1));
@@ -524,13 +524,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             copies_commit();
         };
         State<D> st;
+        ask(0);
         {
             const Heads h0(a, blocks, hpc, p.b, p.y);
             st.load_q(static_cast<const __nv_bfloat16 *>(a.q) + (size_t)h0.row0 * D, h0.n,
                       a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + h0.kvh) : 1.f), lane);
         }
 #pragma unroll 1
-        for (int i = 0; i < S; ++i) ask(i);
+        for (int i = 1; i < S; ++i) ask(i);
         Heads hd(a, blocks, hpc, 0, 0);
         bool fresh = true, began = p.step == 0;
         int valid = 0;
