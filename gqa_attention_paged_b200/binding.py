@@ -8,6 +8,8 @@ missing or the tensors are not on a CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional, Tuple
 
@@ -26,6 +28,7 @@ GQA_MAX_SPLITS = 64
 GQA_SPLITS_BALANCED = -1
 
 _lib = None
+_fast = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
@@ -92,8 +95,23 @@ def load(path: Optional[str] = None):
         fn.restype = res
         fn.argtypes = args
     if path is None:
+        _load_fastcall(lib)
         _lib = lib
     return lib
+
+
+def _load_fastcall(lib):
+    """The compiled half of the hottest functions below (csrc/fastcall.cpp), on this library."""
+    global _fast
+    loader = importlib.machinery.ExtensionFileLoader("_fastcall", _build.FASTCALL)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fastcall", loader))
+    loader.exec_module(module)
+    module.init(torch.Tensor, torch.bfloat16, torch.uint8, torch.float8_e4m3fn, torch.float32,
+                torch.int32, torch.int64,
+                *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+                    "gqa_paged_decode", "gqa_paged_decode_partial", "gqa_paged_append_kv",
+                    "gqa_paged_append_decode", "gqa_paged_write_kv", "gqa_paged_read_kv")))
+    _fast = module
 
 
 def status_string(status: int) -> str:
@@ -105,8 +123,7 @@ def _check(fn: str, status: int):
         raise GQAError(fn, status)
 
 
-# Plain ints, which ctypes converts by the signature: a small decode step is bound by the time
-# this module takes on the host (16.8 -> 9 us a call without c_void_p and Stream objects).
+# Plain ints, which ctypes converts by the signature: c_void_p and Stream objects cost 5 us a call.
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -120,6 +137,22 @@ def _stream(stream) -> int:
             return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _fast_call(fn: str, name: str, args, stream) -> bool:
+    """Call `fn` of the compiled half: True if it was done.  False, with nothing done, for tensors
+    that are not all as the function wants them: the caller's own checks then say what is wrong
+    (or make the call, on tensors that only Python looks through)."""
+    if _fast is None:
+        load()
+    if not torch.cuda.is_initialized():
+        return False
+    st = getattr(_fast, fn)(*args, torch.cuda.current_device(), _stream(stream))
+    if st is None:
+        return False
+    if st != GQA_OK:
+        raise GQAError(name, st)
+    return True
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None, here=None):
@@ -236,6 +269,11 @@ def gqa_paged_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     (uint8/float8_e4m3fn with fp32 scales [num_pages][Hk]), or 4-bit (new_fp4_pool; optional
     fp32 factors [Hk] as k_scale / v_scale); page_table int32 [B][pt_stride];
     seq_lens int32 [B].  Returns (out bf16 [B][Hq][D], lse fp32 [B][Hq] or None)."""
+    if workspace is not None and out is not None and (lse is not None or not want_lse) and \
+            _fast_call("decode", "gqa_paged_decode",
+                       (False, q, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, scale,
+                        num_splits, pack_gqa, out, lse, workspace), stream):
+        return out, lse
     _need(k_pages, "k_pages", _KV_DTYPES)
     kv_dtype, D2 = _kv_layout(k_pages)
     here = _four_bit_device(kv_dtype, k_pages)
@@ -283,6 +321,11 @@ def gqa_paged_decode_partial(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
     """Decode over the tokens page_table / seq_lens cover, as one split's fp32 partial
     result: (o_part fp32 [B][Hq][D] normalised, lse_part fp32 [B][Hq]), the inputs
     lse_combine merges."""
+    if workspace is not None and o_part is not None and lse_part is not None and \
+            _fast_call("decode", "gqa_paged_decode_partial",
+                       (True, q, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, scale,
+                        num_splits, pack_gqa, o_part, lse_part, workspace), stream):
+        return o_part, lse_part
     _need(k_pages, "k_pages", _KV_DTYPES)
     kv_dtype, D2 = _kv_layout(k_pages)
     here = _four_bit_device(kv_dtype, k_pages)
@@ -382,6 +425,11 @@ def gqa_paged_append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch
     """Write token seq_lens[b] - 1 of every sequence (k_new / v_new bf16 [B][Hk][D]) into
     the paged cache, in place (e4m3 and 4-bit pools quantise it; see include/gqa_paged.h).  Returns
     the workspace holding the error word."""
+    if workspace is not None and _fast_call(
+            "append_kv", "gqa_paged_append_kv",
+            (k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, workspace),
+            stream):
+        return workspace
     B, Hk, D, P, num_pages, kv_dtype, here = _append_args(
         k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale)
     if workspace is None:
@@ -407,6 +455,11 @@ def gqa_paged_append_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.T
                             workspace: Optional[torch.Tensor] = None, want_lse: bool = True,
                             stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """gqa_paged_append_kv then gqa_paged_decode on one stream."""
+    if workspace is not None and out is not None and (lse is not None or not want_lse) and \
+            _fast_call("append_decode", "gqa_paged_append_decode",
+                       (q, k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale,
+                        scale, num_splits, pack_gqa, out, lse, workspace), stream):
+        return out, lse
     B, Hk, D, P, num_pages, kv_dtype, here = _append_args(
         k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale)
     _need(q, "q", torch.bfloat16, None, here)
@@ -544,6 +597,11 @@ def gqa_paged_write_kv(k_new: torch.Tensor, v_new: torch.Tensor, cu_q: torch.Ten
     [total_q][Hk][D], rows of any stride; cu_q int32 [B+1]) into the paged cache, in place;
     e4m3 and 4-bit pools quantise them (see include/gqa_paged.h).  Returns the workspace holding
     the error word."""
+    if workspace is not None and _fast_call(
+            "write_kv", "gqa_paged_write_kv",
+            (k_new, v_new, cu_q, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale,
+             max_q_len, workspace), stream):
+        return workspace
     here = _device_of(k_pages)
     kv_dtype, D, num_pages, Hk, P = _pools_on(here, k_pages, v_pages, k_scale, v_scale)
     _need(seq_lens, "seq_lens", torch.int32, None, here)
@@ -578,6 +636,11 @@ def gqa_paged_read_kv(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: 
     bf16, e4m3 or 4-bit pools: (k, v) [total][Hk][D] rows at cu_out (int64 [B+1]), or, with
     `paged`, bf16 pages [total][Hk][P][D] with cu_out counting pages (page cu_out[b] + i holds
     the i-th page of the stretch; slots outside it are not written)."""
+    if workspace is not None and k_out is not None and v_out is not None and _fast_call(
+            "read_kv", "gqa_paged_read_kv",
+            (k_pages, v_pages, page_table, seq_lens, k_scale, v_scale, starts, cu_out, total,
+             paged, k_out, v_out, workspace), stream):
+        return k_out, v_out
     here = _device_of(k_pages)
     kv_dtype, D, num_pages, Hk, P = _pools_on(here, k_pages, v_pages, k_scale, v_scale)
     _need(seq_lens, "seq_lens", torch.int32, None, here)

@@ -18,6 +18,8 @@
 // 8 packed heads N.  The operands code * scale are exact f16 values; q is bf16 scaled per head by
 // a power of two into f16 range (exact but for elements 2^-30 of the head's largest), P is rounded
 // to f16 (2^-11 of each weight, or 2^-32 of the largest); sums, the running reference and the running sum are fp32.
+#include <atomic>
+
 #include "fp4.cuh"
 #include "quant_kv.h"
 
@@ -711,8 +713,17 @@ cudaError_t launch_t(const Fp4DecodeArgs &a, cudaStream_t stream) {
     const int hpc = a.pack_gqa ? (g < kHeads ? g : kHeads) : 1;
     const size_t smem = sizeof(Smem<D>) + 128;
     auto kern = decode_fp4_kernel<D, F32>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // once per device: the call takes as long as a tenth of a small step
+    static std::atomic<uint64_t> ready{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

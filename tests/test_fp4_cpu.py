@@ -173,3 +173,21 @@ def test_model_put_then_read():
             # half the widest gap between codes (4 to 6, one step of the block's scale) and what
             # the e4m3 scale is off by (2^-4 of it, times the code)
             assert np.all(np.abs(y - x[slot]) <= step * (1 + 6 * 2.0 ** -4) + 1e-9)
+
+
+def test_compiled_calls_leave_the_rest_to_python():
+    """Whatever is not a valid call on CUDA tensors returns None and runs nothing."""
+    binding.load()
+    f = binding._fast
+    p = binding.new_fp4_pool(4, 2, 16, 64, "cpu")
+    i32 = torch.zeros(2, 4, dtype=torch.int32)
+    for name, n in (("decode", 16), ("append_kv", 11), ("append_decode", 17), ("write_kv", 13), ("read_kv", 15)):
+        call = getattr(f, name)
+        assert call() is None
+        assert call(*[None] * n) is None
+        assert call(*[None] * (n - 2), 0, 0) is None
+        assert call(*[p] * (n - 2), 0, 0) is None
+        assert call(*[p] * (n - 2), -1, 0) is None
+        assert call(*[i32] * (n - 2), 0, "stream") is None
+    with pytest.raises(TypeError):
+        f.init(1, 2)

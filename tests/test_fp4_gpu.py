@@ -545,6 +545,47 @@ def test_binding_refuses_what_does_not_fit():
     binding.gqa_paged_write_kv(one, one, cu_of([1, 0]), *pools, 1)
 
 
+def test_compiled_calls_take_valid_tensors_only():
+    """The compiled half of the binding makes the calls that Python's checks would make, and no other."""
+    c = Cache([20, 16], 2, 64, 16, seed=3, factor=True).fill()
+    d, q = c.to_gpu(), queries(c, 2, 4).to(DEV)
+    k = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device=DEV)
+    out, lse, ws = torch.empty_like(q), torch.empty(2, 4, device=DEV), binding.new_workspace(1 << 24, DEV)
+    cu, cu64 = cu_of([1, 1]), cu_of([20, 16], torch.int64)
+    rows = torch.empty(36, 2, 64, dtype=torch.bfloat16, device=DEV)
+    pools = [d[n] for n in ("k_pages", "v_pages", "page_table", "seq_lens", "k_scale", "v_scale")]
+    end = (0, torch.cuda.current_stream().cuda_stream)
+    calls = {
+        "decode": [False, q, *pools, 0.1, 0, True, out, lse, ws, *end],
+        "append_kv": [k, k, *pools, ws, *end],
+        "append_decode": [q, k, k, *pools, 0.1, 0, True, out, lse, ws, *end],
+        "write_kv": [k, k, cu, *pools, 1, ws, *end],
+        "read_kv": [*pools, None, cu64, 36, False, rows, rows.clone(), ws, *end],
+    }
+    for name, args in calls.items():
+        f = getattr(binding._fast, name)
+        assert f(*args) == 0, name
+        for i, a in enumerate(args):
+            if not isinstance(a, torch.Tensor):
+                continue
+            wrong = [a.cpu(), a.double() if a.dtype == torch.bfloat16 else a.to(torch.float16), a.unsqueeze(0), "no", 3]
+            if a.dim() > 1:
+                # (rows of any stride are what the chunk write takes)
+                t = a.transpose(0, 1).contiguous().transpose(0, 1) if a.dim() == 2 else a.transpose(-1, -2).contiguous().transpose(-1, -2)
+                wrong.append(t)
+            for w in wrong:
+                assert f(*args[:i], w, *args[i + 1:]) is None, (name, i, type(w))
+            if a.numel() > 300 or a.dim() > 1:
+                continue
+            assert f(*args[:i], torch.cat([a, a]), *args[i + 1:]) is None, (name, i)
+        assert f(*args[:-2], 1, args[-1]) is None
+    # and Python says what the library answers
+    with pytest.raises(binding.GQAError):
+        binding.gqa_paged_decode(q, *pools[:4], 0.1, num_splits=3, out=out, lse=lse, workspace=ws)
+    got, none = binding.gqa_paged_decode(q, *pools[:4], 0.1, out=out, lse=None, workspace=ws, want_lse=False)
+    assert got is out and none is None
+
+
 # ----------------------------------------------------------------------- streams, graphs, all together
 
 def test_decode_in_a_graph_and_on_another_stream():
