@@ -39,7 +39,6 @@ constexpr int kCtasPerSm = 2;
 constexpr int kHeads = 8;  // packed heads of a unit at most: the columns of a product
 constexpr float kNoRef = -3e38f;  // below every reference
 constexpr int kStep = 2 * kFp4Tile;  // tokens of a step: two tiles
-constexpr int kMinSteps = 1;         // steps per warp below which fewer CTAs work
 constexpr int kRuns = kThreads;      // the sequences' step prefix is kept per run of ceil(B / kRuns)
 
 template <int D>
@@ -68,7 +67,7 @@ struct alignas(128) Smem {
     int wsum[kWarps];
     Cut cut[2][kWarps];                             // of head and ring
     int empty[kWarps];
-    int last[2], first[2];
+    int last[2];  // pieces to merge, of the unit begun earlier and of the one begun here
     static_assert(sizeof(float) * C::kDump <= sizeof(ring[0]), "a state fits the warp's ring");
 };
 
@@ -203,6 +202,18 @@ struct Shares {
     }
 };
 
+// The query heads of unit y of sequence b: kv head, first row of q, heads.
+struct Heads {
+    int kvh, row0, n;
+    __device__ __forceinline__ Heads(const Fp4DecodeArgs &a, int blocks, int hpc, int b, int y) {
+        const int g = a.Hq / a.Hk;
+        kvh = blocks == 1 ? y : y / blocks;
+        const int h0 = (y - kvh * blocks) * hpc;
+        n = min(hpc, g - h0);
+        row0 = b * a.Hq + kvh * g + h0;
+    }
+};
+
 // One warp's attention over part of a unit: lane (gq = lane / 4, cq = lane % 4).
 template <int D>
 struct State {
@@ -221,13 +232,28 @@ struct State {
         m[0] = m[1] = l[0] = l[1] = 0.f;
     }
 
-    // `rows`: the unit's n heads; columns past them repeat the first and are never looked at.
-    __device__ __forceinline__ void load_q(const __nv_bfloat16 *rows, int n, float mul, int lane) {
+    // q in two parts: the loads, and what becomes of them.  `rows`: the unit's n heads; the columns
+    // past them are zero and never looked at.
+    struct Query {
+        uint32_t w[D / 8];
+        float mul;
+    };
+    static __device__ __forceinline__ Query fetch_q(const Fp4DecodeArgs &a, const Heads &hd, int lane) {
         const int gq = lane >> 2, cq = lane & 3;
-        const uint4 *src = reinterpret_cast<const uint4 *>(rows + (size_t)(gq < n ? gq : 0) * D + cq * (D / 4));
-        uint32_t w[D / 8], big = 0;
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                           (size_t)(hd.row0 + (gq < hd.n ? gq : 0)) * D + cq * (D / 4));
+        Query x;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) *reinterpret_cast<uint4 *>(w + 4 * i) = gq < n ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < D / 32; ++i)
+            *reinterpret_cast<uint4 *>(x.w + 4 * i) = gq < hd.n ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        x.mul = a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + hd.kvh) : 1.f);
+        return x;
+    }
+
+    __device__ __forceinline__ void set_q(const Query &x, int lane) {
+        const int cq = lane & 3;
+        const uint32_t(&w)[D / 8] = x.w;
+        uint32_t big = 0;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) big = __vmaxu2(big, w[i] & 0x7fff7fffu);
         big = __vmaxu2(big, __shfl_xor_sync(kFull, big, 1));
@@ -238,8 +264,8 @@ struct State {
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
             qf[i / 2][i & 1] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
-        kmul[0] = mul * __shfl_sync(kFull, down, 8 * cq);
-        kmul[1] = mul * __shfl_sync(kFull, down, 8 * cq + 4);
+        kmul[0] = x.mul * __shfl_sync(kFull, down, 8 * cq);
+        kmul[1] = x.mul * __shfl_sync(kFull, down, 8 * cq + 4);
     }
 
     // The products q k of a step's two tiles; its values into registers.
@@ -400,18 +426,6 @@ __device__ __forceinline__ void store_dims(void *out, size_t idx, const float (&
     }
 }
 
-// The query heads of unit y of sequence b: kv head, first row of q, heads.
-struct Heads {
-    int kvh, row0, n;
-    __device__ __forceinline__ Heads(const Fp4DecodeArgs &a, int blocks, int hpc, int b, int y) {
-        const int g = a.Hq / a.Hk;
-        kvh = blocks == 1 ? y : y / blocks;
-        const int h0 = (y - kvh * blocks) * hpc;
-        n = min(hpc, g - h0);
-        row0 = b * a.Hq + kvh * g + h0;
-    }
-};
-
 template <int D, bool F32>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_fp4_kernel(const Fp4DecodeArgs a, const int hpc, const int blocks) {
@@ -469,12 +483,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
     }
     // CTAs with work
-    const int NC = max(1, min((int)gridDim.x, T / (kWarps * kMinSteps)));
+    const int NC = max(1, min((int)gridDim.x, T / kWarps));
     if (T == 0 || blockIdx.x >= NC) return;
 
     // ---- this warp's share: steps [s_w, s_w + n)
     Shares sh;
-    sh.q = (unsigned)T / (unsigned)(NC * kWarps);
+    // (below the whole grid NC is T / kWarps: a step each, and one more for some)
+    sh.q = NC == (int)gridDim.x ? (int)((unsigned)T / (gridDim.x * kWarps)) : (T >= kWarps ? 1 : 0);
     sh.rem = T - sh.q * (NC * kWarps);
     const int s_w = sh.start(blockIdx.x * kWarps + warp);
     const int n = sh.start(blockIdx.x * kWarps + warp + 1) - s_w;
@@ -525,13 +540,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
             copies_commit();
         };
+        // the first q sets out before the first keys, and is looked at between the first asks
         State<D> st;
+        const auto q0 = State<D>::fetch_q(a, Heads(a, blocks, hpc, p.b, p.y), lane);
         ask(0);
-        {
-            const Heads h0(a, blocks, hpc, p.b, p.y);
-            st.load_q(static_cast<const __nv_bfloat16 *>(a.q) + (size_t)h0.row0 * D, h0.n,
-                      a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + h0.kvh) : 1.f), lane);
-        }
+        st.set_q(q0, lane);
 #pragma unroll 1
         for (int i = 1; i < S; ++i) ask(i);
         Heads hd(a, blocks, hpc, 0, 0);
@@ -543,8 +556,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 hd = Heads(a, blocks, hpc, p.b, p.y);
                 valid = bt.len(p.b) - p.step * kStep;
                 st.reset();
-                if (r > 0) st.load_q(static_cast<const __nv_bfloat16 *>(a.q) + (size_t)hd.row0 * D, hd.n,
-                          a.scale * kLog2e * (a.k_scale ? __ldg(a.k_scale + hd.kvh) : 1.f), lane);
+                if (r > 0) st.set_q(State<D>::fetch_q(a, hd, lane), lane);
             }
             copies_wait<S - 1>();
             __syncwarp();
@@ -605,8 +617,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             if (k > w0 && sm.cut[0][k].unit == tc.unit) has |= 1u << k;
         has |= 1u << w0;
     }
-    // does the unit go on in other CTAs?
+    // does the unit go on in other CTAs?  From which to which?
     const bool cross = tc.unit >= 0 && (tc.first < c_start || tc.first + tc.steps > c_end);
+    const int c0 = cross ? sh.owner(tc.first) / kWarps : 0, c1 = cross ? sh.owner(tc.first + tc.steps - 1) / kWarps : 0;
     const unsigned crossing = __ballot_sync(kFull, cross);
     auto put = [&](int row, int kvh, const float(&acc)[V], float M, float L) {
         const float vf = a.v_scale ? __ldg(a.v_scale + kvh) : 1.f;
@@ -655,26 +668,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // arrive merges the pieces
     __syncthreads();
     if (warp == 0 && cross) {
-        const int side = lane > 0, c0 = sh.owner(tc.first) / kWarps, c1 = sh.owner(tc.first + tc.steps - 1) / kWarps;
-        __threadfence();
-        int last = 0;
-        if (atomicAdd(a.counters + tc.unit, 1) == c1 - c0) {
-            a.counters[tc.unit] = 0;  // ready for the next launch
-            last = c1 - c0 + 1;
-        }
-        __threadfence();
-        sm.first[side] = c0;
-        sm.last[side] = last;
+        // (release: the CTA's pieces, by way of the barrier; acquire: those of the CTAs before)
+        int before;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.counters + tc.unit) : "memory");
+        const bool last = before == c1 - c0;
+        if (last) a.counters[tc.unit] = 0;  // ready for the next launch
+        sm.last[lane > 0] = last ? c1 - c0 + 1 : 0;
     }
     __syncthreads();
 #pragma unroll 1
     for (unsigned left = crossing; left; left &= left - 1) {
-        const int t = __ffs(left) - 1, np = sm.last[t > 0], c0 = sm.first[t > 0];
+        const int t = __ffs(left) - 1, np = sm.last[t > 0], from = __shfl_sync(kFull, c0, t);
         if (np == 0) continue;
         const int heads = __shfl_sync(kFull, tc.n, t), row0 = __shfl_sync(kFull, tc.row0, t);
         const int kvh = __shfl_sync(kFull, tc.kvh, t);
         // begun in the unit's first CTA (piece 1), carried on in the others (piece 0)
-        auto piece = [&](int k) { return a.pieces + ((size_t)(c0 + k) * 2 + (k == 0)) * slot_floats; };
+        auto piece = [&](int k) { return a.pieces + ((size_t)(from + k) * 2 + (k == 0)) * slot_floats; };
 #pragma unroll 1
         for (h = warp; h < heads; h += kWarps) {
             float M = kNoRef, L = 0.f, acc[V] = {};
