@@ -145,9 +145,15 @@ def _fast_call(fn: str, name: str, args, stream) -> bool:
     (or make the call, on tensors that only Python looks through)."""
     if _fast is None:
         load()
-    if not torch.cuda.is_initialized():
+    try:
+        here = torch.cuda.current_device()
+    except (RuntimeError, AssertionError):  # no GPU, or a torch without CUDA
         return False
-    st = getattr(_fast, fn)(*args, torch.cuda.current_device(), _stream(stream))
+    if stream is None and _raw_stream is not None:
+        stream = _raw_stream(here)
+    else:
+        stream = _stream(stream)
+    st = getattr(_fast, fn)(*args, here, stream)
     if st is None:
         return False
     if st != GQA_OK:

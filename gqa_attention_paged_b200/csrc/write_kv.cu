@@ -247,12 +247,26 @@ __global__ void __launch_bounds__(kThreads, 4) write_page_kernel(const WriteArgs
         float s = 1.f;
         if (FP8) {
             float *scales = is_v ? a.v_scale : a.k_scale;
+            // magnitudes order as integers, two at once; a NaN, which the scale takes no notice of, is
+            // above infinity
+            uint32_t big = 0;
 #pragma unroll
             for (int i = 0; i < kIts; ++i) {
-                float x[8];
-                unpack_bf16x8(w[i], x);
+                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[k]));
+                for (int k = 0; k < 4; ++k) big = __vmaxu2(big, u[k] & 0x7fff7fffu);
+            }
+            big = max(big >> 16, big & 0xffffu);
+            m = __uint_as_float(big << 16);
+            if (big > 0x7f80u) {
+                m = 0.f;
+#pragma unroll
+                for (int i = 0; i < kIts; ++i) {
+                    float x[8];
+                    unpack_bf16x8(w[i], x);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[k]));
+                }
             }
             if (pg.slot == 0) {
 #pragma unroll
