@@ -250,7 +250,7 @@ int decode_call(const void *q, const void *k_pages, const void *v_pages, const f
         f.lse = lse;
         f.err = reinterpret_cast<int *>(ws);
         f.counters = reinterpret_cast<int *>(ws + kWorkspaceHeader);
-        f.pieces = reinterpret_cast<float *>(ws + decode_zero_prefix_bytes(B, Hq));
+        f.pieces = reinterpret_cast<float *>(ws + fp4_decode_zero_bytes());
         f.sms = sm_count() > kStreamMaxSms ? kStreamMaxSms : sm_count();
         return launch_decode_fp4(f, stream) == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
     }
@@ -334,7 +334,7 @@ size_t gqa_paged_decode_workspace_size(int B, int Hq, int Hk, int head_dim, int 
     if (kv_dtype == GQA_KV_FP4)
         return B < 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0
                    ? kWorkspaceHeader
-                   : decode_zero_prefix_bytes(B, Hq) + fp4_decode_piece_bytes(Hq, Hk, head_dim);
+                   : fp4_decode_zero_bytes() + fp4_decode_piece_bytes(Hq, Hk, head_dim);
     const int S = decode_schedule(num_splits, B, Hk, max_seq_len, page_size, kv_dtype);
     if (S == 0 && Hq > 0 && Hk > 0 && Hq % Hk == 0)
         return decode_zero_prefix_bytes(B, Hq) + stream_k_piece_bytes(Hq, Hk, head_dim);

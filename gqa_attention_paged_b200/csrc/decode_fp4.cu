@@ -668,11 +668,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // arrive merges the pieces
     __syncthreads();
     if (warp == 0 && cross) {
+        // one counter per CTA that such a unit begins in: no CTA has two
         // (release: the CTA's pieces, by way of the barrier; acquire: those of the CTAs before)
         int before;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.counters + tc.unit) : "memory");
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.counters + c0) : "memory");
         const bool last = before == c1 - c0;
-        if (last) a.counters[tc.unit] = 0;  // ready for the next launch
+        if (last) a.counters[c0] = 0;  // ready for the next launch
         sm.last[lane > 0] = last ? c1 - c0 + 1 : 0;
     }
     __syncthreads();
@@ -748,7 +749,11 @@ cudaError_t launch_t(const Fp4DecodeArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
-// Two pieces per CTA of the largest grid.
+// A counter per CTA of the largest grid, at a place that no batch size or head count moves: a
+// workspace that was zeroed once serves them all.
+size_t fp4_decode_zero_bytes() { return kWorkspaceHeader + (size_t)kStreamMaxSms * kCtasPerSm * sizeof(int); }
+
+// Two pieces per CTA.
 size_t fp4_decode_piece_bytes(int Hq, int Hk, int D) {
     const int g = Hq / Hk, hpc = g < kHeads ? g : kHeads;
     return (size_t)kStreamMaxSms * kCtasPerSm * 2 * hpc * (D + 2) * sizeof(float);

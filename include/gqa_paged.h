@@ -104,7 +104,10 @@ typedef enum {
  * Bytes of workspace gqa_paged_decode() needs for the same B, heads, head_dim, page_size,
  * longest context (pt_stride * page_size), kv_dtype and num_splits.  Layout: a 256-byte
  * header holding the device error word, then
- *   GQA_KV_FP4: int32 merge counters [B*Hq] (rounded up to 256 bytes) and the merge pieces;
+ *   GQA_KV_FP4: int32 merge counters [160 SMs x 2 CTAs] and the merge pieces, 2 per CTA, each
+ *     min(Hq/Hk, 8) x (head_dim + 2) fp32.  The counters' place depends on nothing, so that a
+ *     workspace zeroed once and large enough serves any batch size and head count; one that
+ *     served other pools' decode calls is zeroed before;
  *   num_splits = 0, B <= 2048 (balanced schedule): int32 merge counters [B*Hq] (rounded
  *     up to 256 bytes) and the merge pieces, 2 per worker of the largest grid
  *     (160 SMs x 2 CTAs x 4 workers), each min(Hq/Hk, 16) x (head_dim + 1) fp32;

@@ -94,8 +94,9 @@ def test_host_policy():
     lib = binding.load()
     ws = lib.gqa_paged_decode_workspace_size
     for B in (1, 64, 5000, 65535):
-        # the same for every context and for the two names of the one schedule; room for the counters
-        assert ws(B, 32, 8, 128, 16, 2048, 2, 0) == ws(B, 32, 8, 128, 64, 32768, 2, -1) >= 256 + 4 * B * 32
+        # the same for every batch, context and for the two names of the one schedule; room for a counter
+        # and two pieces of 4 heads of every CTA
+        assert ws(B, 32, 8, 128, 16, 2048, 2, 0) == ws(1, 32, 8, 128, 64, 32768, 2, -1) >= 256 + 320 * (4 + 2 * 4 * 130 * 4)
     assert ws(64, 64, 2, 128, 16, 2048, 2, 0) <= binding.new_workspace(16 << 20, "cpu").numel()
     assert lib.gqa_pick_splits(1, 8, 32768, 16, 2) == 1
     assert binding.gqa_paged_decode_kernel_launches(4, 64, 8, 128, 64, 32768, 2, 0) == 1

@@ -252,6 +252,50 @@ def test_write_refuses_what_does_not_fit(kv):
                 assert np.array_equal(bits(d[name])[c.table[1, :2]], before[i][c.table[1, :2]]), bad
 
 
+def test_write_of_many_sequences():
+    """More sequences than a CTA keeps one by one; chunks of none to a few tokens."""
+    r = rng(17)
+    counts = [int(x) for x in r.integers(0, 4, 300)]
+    lens = [n + int(x) for n, x in zip(counts, r.integers(0, 20, 300))]
+    for kv in ("fp4", "e4m3"):
+        c = Cache(lens, 1, 64, 16, kv, seed=18)
+        check_write(c, counts, *rows_for(c, counts))
+
+
+def test_quotients_are_a_divisions():
+    """e4m3 codes under given page scales: bf16 values at and around every tie of the codes, over scales whose
+    quotients come closest to one (24-bit integers next to multiples of 2^20), random ones, and ones at the
+    ends of the range, negative and zero."""
+    r = rng(19)
+    near = [(k << 20) + d for k in range(8, 16) for d in range(-4, 5)]
+    s = [np.float32(x) * np.float32(2.0) ** int(e) for x, e in zip(near, r.integers(-40, 20, len(near)))]
+    s += list(r.uniform(0.5, 2, 60).astype(np.float32) * np.exp2(r.integers(-30, 30, 60)).astype(np.float32))
+    s += [np.float32(x) for x in (0, 1e-45, 3e-41, 1.2e-38, 2.0 ** -61, 2.0 ** 61, 1e30, 3e38, -0.37, -1e-20)]
+    s = np.array(s, np.float32)
+    n = len(s)
+    ties = np.concatenate([(M.E4M3[1:] + M.E4M3[:-1]) / 2, M.E4M3[1:], [480.0, 1e6, 1e30]])
+    with np.errstate(over="ignore"):
+        t = np.abs(s.astype(np.float64))[:, None] * r.choice(ties, (n, 1920)) * (1 + r.choice([0, 1, -1], (n, 1920)) * 2.0 ** -8)
+    x = np.clip(t, 2.0 ** -126, 3e38) * r.choice([1, -1], (n, 1920))
+    x[:, 0], x[:, 1] = 0.0, -0.0
+    x = bf16(x)
+    xs = x.double().numpy()
+    with np.errstate(all="ignore"):
+        y = (xs.astype(np.float32) / s[:, None]).astype(np.float64)
+    keep = ~np.isnan(y)  # 0 / 0
+    want = M.e4m3_code(np.where(keep, y, 0.0))
+    pages = [torch.zeros(n, 1, 16, 128, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    scales = [dev(s[:, None]), dev(s[:, None])]
+    table = torch.arange(n, dtype=torch.int32, device=DEV)[:, None].contiguous()
+    rows = x.view(n * 15, 1, 128).to(DEV)
+    binding.gqa_paged_write_kv(rows, rows, cu_of([15] * n), *pages, table, torch.full((n,), 16, dtype=torch.int32, device=DEV),
+                               15, k_scale=scales[0], v_scale=scales[1])
+    for p, sc in zip(pages, scales):
+        got = p[:, 0, 1:].reshape(n, 1920).cpu().numpy()
+        assert np.array_equal(got[keep], want[keep]), np.argwhere((got != want) & keep)[:5]
+        assert np.array_equal(sc.cpu().numpy()[:, 0], s)
+
+
 # ------------------------------------------------------------------------------------ reading
 
 @pytest.mark.parametrize("kv", ["fp4", "e4m3", "bf16"])
@@ -373,6 +417,51 @@ def test_decode_matches_the_model(case):
     close(part, lsep, ref, f32_out=True)
     stat, lses = binding.gqa_paged_decode_static_scratch(q.to(DEV), scale=scale, **d)
     assert torch.equal(stat.view(torch.int16), out.view(torch.int16)) and torch.equal(lses, lse)
+
+
+@pytest.mark.parametrize("B,per", [(257, 7), (700, 40)])
+def test_decode_of_many_sequences(B, per):
+    """More sequences than the kernel keeps one by one: runs of them, empty ones inside and at the ends."""
+    r = rng(B)
+    lens = [int(x) if x > 2 else 0 for x in r.integers(0, per, B)]
+    lens[0] = lens[-1] = lens[255] = 0
+    c = Cache(lens, 1, 64, 16, seed=B).fill()
+    q, scale = queries(c, B, 2), 0.125
+    out, lse = binding.gqa_paged_decode(q.to(DEV), scale=scale, **c.to_gpu())
+    close(out, lse, expect(c, q, scale))
+
+
+def test_one_workspace_for_changing_batches():
+    """Batch sizes and head counts in turn on one workspace that was zeroed once."""
+    ws = binding.new_workspace(16 << 20, DEV)
+    shapes = [([300], 8, 2, 128), ([200, 90, 310] * 4, 8, 2, 128), ([700], 16, 1, 64), ([5] * 40 + [400], 4, 2, 128)]
+    batches = []
+    for i, (lens, Hq, Hk, D) in enumerate(shapes):
+        c = Cache(lens, Hk, D, 16, seed=70 + i).fill()
+        q = queries(c, len(lens), Hq)
+        batches.append((c.to_gpu(), q.to(DEV), expect(c, q, 0.1)))
+    for i in (0, 1, 2, 3, 1, 0, 3, 2):
+        d, q, ref = batches[i]
+        out, lse = binding.gqa_paged_decode(q, scale=0.1, workspace=ws, **d)
+        close(out, lse, ref)
+    assert binding.gqa_get_error(ws) == 0
+
+
+def test_two_decodes_at_once():
+    """Two streams, a workspace each."""
+    c = Cache([900, 300], 2, 128, 16, seed=81).fill()
+    d, ref = c.to_gpu(), None
+    q = queries(c, 2, 8)
+    ref, qd = expect(c, q, 0.1), q.to(DEV)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    bufs = [(torch.empty_like(qd), torch.empty(2, 8, device=DEV), binding.new_workspace(4 << 20, DEV)) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (out, lse, ws) in zip(streams, bufs):
+            binding.gqa_paged_decode(qd, scale=0.1, out=out, lse=lse, workspace=ws, stream=s, **d)
+    torch.cuda.synchronize()
+    for out, lse, ws in bufs:
+        close(out, lse, ref)
 
 
 @pytest.mark.parametrize("what", ["large q", "small q", "mixed heads", "large scale", "negative scale", "zero scale"])
