@@ -1,7 +1,9 @@
 // write_kv.cu -- writes the newest tokens of every sequence into the paged cache: a prefill
 // chunk's, or a decode step's one token ("TensorRT对Grouped Query Attention的支持进展", sections
 // "动态形状与KV Cache管理" and "与动态批处理协同"), quantised on the way for 4-bit and e4m3 pools.
-// Bound by HBM (16 bits in, 4 to 16 out).  The grid runs over the rows of the input, so that no CTA
+// Bound by HBM (16 bits in, 4 to 16 out) and, as it stands, by the look-ups before a CTA's first
+// load: 4096 tokens into 4-bit pages 7.4 us (21 MB), 15421 ragged ones into 4-bit pages 21 us
+// (3.8 TB/s), into e4m3 pages 24 us (3.9 TB/s).  The grid runs over the rows of the input, so that no CTA
 // is idle however ragged the chunks are; a thread per row first finds where the row goes.
 //
 // 4-bit pools (write_fp4_kernel).  A block of 16 dims of one token, with g the head's factor:
