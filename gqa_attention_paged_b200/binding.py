@@ -106,8 +106,7 @@ def _load_fastcall(lib):
     loader = importlib.machinery.ExtensionFileLoader("_fastcall", _build.FASTCALL)
     module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fastcall", loader))
     loader.exec_module(module)
-    module.init(torch.Tensor, torch.bfloat16, torch.uint8, torch.float8_e4m3fn, torch.float32,
-                torch.int32, torch.int64,
+    module.init(torch.Tensor,
                 *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
                     "gqa_paged_decode", "gqa_paged_decode_partial", "gqa_paged_append_kv",
                     "gqa_paged_append_decode", "gqa_paged_write_kv", "gqa_paged_read_kv")))
@@ -129,6 +128,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream) -> int:
@@ -146,14 +146,10 @@ def _fast_call(fn: str, name: str, args, stream) -> bool:
     if _fast is None:
         load()
     try:
-        here = torch.cuda.current_device()
-    except (RuntimeError, AssertionError):  # no GPU, or a torch without CUDA
+        here = _get_device()
+    except (RuntimeError, AssertionError):  # no GPU
         return False
-    if stream is None and _raw_stream is not None:
-        stream = _raw_stream(here)
-    else:
-        stream = _stream(stream)
-    st = getattr(_fast, fn)(*args, here, stream)
+    st = getattr(_fast, fn)(*args, here, None if stream is None else _stream(stream))
     if st is None:
         return False
     if st != GQA_OK:

@@ -1,6 +1,7 @@
 """Build libgqa_paged.so (the sm_100a CUDA library behind include/gqa_paged.h) in-tree
 with nvcc.  `python -m gqa_attention_paged_b200.build [--force]`."""
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
@@ -17,6 +18,12 @@ CXX = os.environ.get("CXX", "g++")
 
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-Xptxas", "-v"]
+
+
+def _torch_include():
+    """Of torch's headers only the DLPack one is used, which includes nothing of torch."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.join(os.path.dirname(spec.origin), "include")
 
 
 def sources():
@@ -57,7 +64,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = FASTCALL + f".tmp{os.getpid()}"
     cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", "-I", INCLUDE, "-I",
            os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), "-I",
-           sysconfig.get_paths()["include"], os.path.join(CSRC, "fastcall.cpp"), "-o", tmp]
+           sysconfig.get_paths()["include"], "-I", _torch_include(),
+           os.path.join(CSRC, "fastcall.cpp"), "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{CXX} failed on fastcall.cpp:\n{r.stdout}\n{r.stderr}")

@@ -192,3 +192,5 @@ def test_compiled_calls_leave_the_rest_to_python():
         assert call(*[i32] * (n - 2), 0, "stream") is None
     with pytest.raises(TypeError):
         f.init(1, 2)
+    with pytest.raises(ValueError):
+        f.init(torch.Tensor, 0, 0, 0, 0, 0, 0)
