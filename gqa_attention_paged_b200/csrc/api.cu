@@ -78,10 +78,10 @@ bool known_kv_dtype(int t) {
     return t == GQA_KV_BF16 || t == GQA_KV_FP8_E4M3 || t == GQA_KV_FP4;
 }
 
-// The 4-bit decode counts the batch's steps of 32 tokens in an int.
+// The 4-bit decode counts the batch's steps of 32 tokens, and one more for each head, in an int.
 bool fp4_steps_fit(int B, int Hq, int pt_stride, int P) {
     const int64_t rows = (int64_t)B * Hq;
-    return rows <= INT32_MAX && rows * (((int64_t)pt_stride * P + 31) / 32) <= INT32_MAX;
+    return rows <= INT32_MAX && rows * (((int64_t)pt_stride * P + 31) / 32 + 1) <= INT32_MAX;
 }
 
 int sm_count();

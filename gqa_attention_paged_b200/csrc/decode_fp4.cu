@@ -6,8 +6,10 @@
 // once; the softmax is the online form ("TensorRT-LLM与TensorRT核心差异解析", section 4.2.1).
 //
 // Schedule.  The 32-token steps of all (sequence, kv head [, block of heads]) units are laid end
-// to end and cut into equal contiguous shares, one per warp of a fixed grid.  A warp streams its
-// share through a private shared-memory ring of 16-byte asynchronous copies (a tile's codes and
+// to end and cut into equal contiguous shares, one per warp of a fixed grid.  Going on to a unit (its
+// q, the last one's results) takes as long as a step, so with several steps a warp a unit counts one
+// place more than its steps; without that, warps with many short units came last (64 sequences of
+// 0 .. 4096 tokens: 43.0 us, 38.5 with it).  A warp streams its share through a private shared-memory ring of 16-byte asynchronous copies (a tile's codes and
 // scales are contiguous; a bulk copy per tile, 1152 bytes, was bound by the copies an SM can
 // start, about one in 32 cycles): the step is taken into registers and its slot handed to the step
 // kStages further on.  No warp waits for another until the end.  Units cut between the warps of a
@@ -19,12 +21,12 @@
 // a power of two into f16 range (exact but for elements 2^-30 of the head's largest), P is rounded
 // to f16 (2^-11 of each weight, or 2^-32 of the largest); sums, the running reference and the
 // running sum are fp32.  Groups above 8 run as blocks of 8 heads, whose second read of a tile is an
-// L2 hit (groups of 16, 48 x 0 .. 3000 tokens: 30.6 us; one block of 16 heads, 35.6).
+// L2 hit (groups of 16, 48 x 0 .. 3000 tokens: 26.8 us; one block of 16 heads took 5 more).
 //
 // What bounds it.  A step of 32 tokens is 561 instructions a warp, 128 conversions and 128 scale
 // multiplications among them, 96 us of arithmetic at 256 x 2048 tokens and 8 kv heads where the
-// copies alone take 98; together 109 us (607 MB, 5.6 TB/s), 126 once the power cap holds the clock.
-// 64 x 2048: 37 us, of which 3 go before the first keys and 4 into the merges; 1 x 2048: 9.8 us.
+// copies alone take 98; together 112 us (607 MB, 5.4 TB/s), 128 once the power cap holds the clock.
+// 64 x 2048: 37 us, of which 3 go before the first keys and 4 into the merges; 1 x 2048: 10 us.
 #include <atomic>
 
 #include "fp4.cuh"
@@ -46,6 +48,10 @@ constexpr int kCtasPerSm = 2;
 constexpr int kHeads = 8;  // packed heads of a unit at most: the columns of a product
 constexpr float kNoRef = -3e38f;  // below every reference
 constexpr int kStep = 2 * kFp4Tile;  // tokens of a step: two tiles
+// Steps a warp from which on a unit counts one place more than its steps.  Ragged lengths, us without
+// and with: 13 steps a warp 34.3 and 28.8, 7.1 30.5 and 26.9, 4.2 19.8 and 20.3, 2.0 14.9 and 15.3;
+// uniform ones 1% slower with it (64 x 2048: 36.9 and 37.1).
+constexpr int kWeighted = 5;
 constexpr int kRuns = kThreads;      // the sequences' step prefix is kept per run of ceil(B / kRuns)
 
 template <int D>
@@ -58,8 +64,8 @@ struct Cfg {
     static constexpr int kDump = kHeads * (RS + 2);  // floats: O rows, then m and l
 };
 
-// The unit that a dumped state belongs to (-1: no state): its first step in the batch's order, its
-// steps, kv head, first row of q and heads.
+// The unit that a dumped state belongs to (-1: no state): the place of its first step, its steps, kv
+// head, first row of q and heads.
 struct Cut {
     int unit, first, steps, kvh, row0, n;
 };
@@ -124,15 +130,19 @@ __device__ __forceinline__ int clamped(const Fp4DecodeArgs &a, int L) {
 __device__ __forceinline__ int clamped_len(const Fp4DecodeArgs &a, int b) { return clamped(a, __ldg(a.seq_lens + b)); }
 __device__ __forceinline__ int steps_of(int L) { return (int)(((unsigned)L + kStep - 1) / kStep); }
 
+__device__ __forceinline__ bool weighted(int total) { return total >= kWeighted * kWarps * (int)gridDim.x; }
+
 // The batch as every warp sees it: units of a sequence, sequences of a run, and in shared memory
-// the steps before each run (times U: the flat index of its first step) and the lengths.  The host
-// keeps all step indices within an int.
+// the steps before each run (times U: flat indices) and the lengths.  A unit has `more` (0 or 1)
+// places beyond its steps; for want of a second prefix the units of an empty sequence have them too.
+// The host keeps all of these within an int.
 struct Batch {
     const Fp4DecodeArgs &a;
     const int *pre, *lens;
-    int U, per;
+    int U, per, more;
     __device__ __forceinline__ int len(int b) const { return per == 1 ? lens[b] : clamped_len(a, b); }
     __device__ __forceinline__ int steps(int b) const { return steps_of(len(b)); }
+    __device__ __forceinline__ int place(int run) const { return U * (pre[run] + more * min(run * per, a.B)); }
 };
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -164,42 +174,64 @@ __device__ __forceinline__ void advance(Pos &p, int n, const Batch &bt) {
     p.step = flat - p.y * p.nt;
 }
 
-// The place of step f (a whole warp calls it with the same f).
-__device__ __forceinline__ Pos locate(int f, const Batch &bt, int lane) {
+// The step at place f or, where that is a unit's extra place, the next one (a whole warp calls it with
+// the same f).  `index`: the step's flat index, the number of steps if there is none.
+__device__ __forceinline__ Pos locate(int f, const Batch &bt, int lane, int &index) {
     // the first run that ends behind f, by its eighth and then its place there
     static_assert(kRuns == 256, "32 lanes of 8 runs");
-    int run = (__ffs(__ballot_sync(kFull, bt.U * bt.pre[8 * lane + 8] > f)) - 1) * 8;
-    run += __ffs(__ballot_sync(kFull, bt.U * bt.pre[run + (lane & 7) + 1] > f)) - 1;
-    unsigned local = f - bt.U * bt.pre[run];
-    int b = run * bt.per;
+    int run = (__ffs(__ballot_sync(kFull, bt.place(8 * lane + 8) > f)) - 1) * 8;
+    run += __ffs(__ballot_sync(kFull, bt.place(run + (lane & 7) + 1) > f)) - 1;
+    unsigned local = f - bt.place(run);
+    int b = run * bt.per, before = bt.pre[run];
     if (bt.per > 1) {
         for (const int end = min(bt.a.B, b + bt.per); b < end; b += 32) {
-            const int nt = b + lane < end ? bt.steps(b + lane) : 0;
-            int incl = nt;
+            const int places = b + lane < end ? bt.steps(b + lane) + bt.more : 0;
+            int incl = places;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int t = __shfl_up_sync(kFull, incl, o);
                 if (lane >= o) incl += t;
             }
             const unsigned past = __ballot_sync(kFull, (unsigned)(bt.U * incl) > local);
+            const int src = past ? __ffs(past) - 1 : 32;
+            const int skipped = __shfl_sync(kFull, past ? incl - places : incl, src & 31);
+            const int all = past ? skipped : __shfl_sync(kFull, incl, 31);
+            local -= bt.U * all;
+            before += all - bt.more * src;
             if (past) {
-                const int src = __ffs(past) - 1;
-                local -= bt.U * __shfl_sync(kFull, incl - nt, src);
                 b += src;
                 break;
             }
-            local -= bt.U * __shfl_sync(kFull, incl, 31);
         }
     }
-    Pos p;
-    p.b = b;
-    p.nt = bt.steps(b);
-    p.y = local / p.nt;
-    p.step = local - p.y * p.nt;
+    Pos p = {b, 0, 0, bt.steps(b)};
+    if (p.nt == 0) {  // of an empty sequence
+#pragma unroll 1
+        do
+            if (++p.b >= bt.a.B) {
+                index = bt.U * bt.pre[kRuns];
+                return {bt.a.B - 1, 0, 0, 1};
+            }
+        while ((p.nt = bt.steps(p.b)) == 0);
+    } else {
+        p.y = local / (p.nt + bt.more);
+        p.step = max((int)(local - p.y * (p.nt + bt.more)) - bt.more, 0);
+    }
+    index = bt.U * before + p.y * p.nt + p.step;
     return p;
 }
 
-// The batch's steps in equal shares, the first `rem` of them one longer.
+// The place of the first step of p's unit.
+__device__ __forceinline__ int first_place(const Batch &bt, const Pos &p, int more) {
+    const int run = bt.per == 1 ? p.b : p.b / bt.per;
+    int before = bt.pre[run];
+    if (bt.per > 1)
+#pragma unroll 1
+        for (int b = run * bt.per; b < p.b; ++b) before += bt.steps(b);
+    return bt.U * (before + more * p.b) + p.y * (p.nt + more) + more;
+}
+
+// The batch's places in equal shares, the first `rem` of them one longer.
 struct Shares {
     int q, rem;
     __device__ __forceinline__ int start(int w) const { return w * q + min(w, rem); }
@@ -442,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     Smem<D> &sm = *reinterpret_cast<Smem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int U = a.Hk * blocks;
-    const Batch bt = {a, sm.pre, sm.len, U, a.B <= kRuns ? 1 : (a.B + kRuns - 1) / kRuns};
+    Batch bt = {a, sm.pre, sm.len, U, a.B <= kRuns ? 1 : (a.B + kRuns - 1) / kRuns, 0};
 
     // launched with programmatic stream serialization: nothing below reads or writes before the
     // previous kernel of the stream is complete
@@ -475,7 +507,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (threadIdx.x == 0) sm.pre[0] = 0;
         none = __syncthreads_or(none);
     }
-    const int T = U * sm.pre[kRuns];
+    const int total = U * sm.pre[kRuns];
+    bt.more = weighted(total);
+    const int T = total + bt.more * U * a.B;
 
     if (none) {  // zeros and -inf
         const float zero[4] = {};
@@ -493,20 +527,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int NC = max(1, min((int)gridDim.x, T / kWarps));
     if (T == 0 || blockIdx.x >= NC) return;
 
-    // ---- this warp's share: steps [s_w, s_w + n)
+    // ---- this warp's share: n steps from place s_w on
     Shares sh;
     // (below the whole grid NC is T / kWarps: a step each, and one more for some)
     sh.q = NC == (int)gridDim.x ? (int)((unsigned)T / (gridDim.x * kWarps)) : (T >= kWarps ? 1 : 0);
     sh.rem = T - sh.q * (NC * kWarps);
-    const int s_w = sh.start(blockIdx.x * kWarps + warp);
-    const int n = sh.start(blockIdx.x * kWarps + warp + 1) - s_w;
+    const int s_w = sh.start(blockIdx.x * kWarps + warp), e_w = sh.start(blockIdx.x * kWarps + warp + 1);
+    int n = e_w - s_w, index = 0;
+    Pos p = {a.B - 1, 0, 0, 1};
+    if (n > 0) p = locate(s_w, bt, lane, index);
+    if (bt.more) {
+        int end = total;
+        if (e_w < T) locate(e_w, bt, lane, end);
+        n = end - index;
+    }
     if (lane < 2) sm.cut[lane][warp].unit = -1;
-    if (lane == 0) sm.empty[warp] = n == 0;
+    if (lane == 0) {
+        sm.empty[warp] = n == 0;
+    }
     __syncwarp();
     if (n > 0) {
         const uint64_t policy = policy_evict_first();
         const int tshift = a.P == 16 ? 0 : (a.P == 32 ? 1 : 2);  // tiles of a page: 1, 2 or 4
-        Pos p = locate(s_w, bt, lane);
         // window of 32 steps: lane i holds the place and the pool tiles of the share's step 32 w + i
         // (-1: none)
         Pos wp = p;
@@ -593,13 +635,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             } else {
                 // a share that ends inside the unit: the ring is free, no copy is in flight
                 st.dump(began ? reinterpret_cast<float *>(sm.ring[warp]) : sm.head[warp], lane);
-                if (lane == 0) sm.cut[began][warp] = {p.b * U + p.y, s_w + r + 1 - p.step, p.nt, hd.kvh, hd.row0, hd.n};
+                if (lane == 0) sm.cut[began][warp] = {p.b * U + p.y, first_place(bt, p, bt.more), p.nt, hd.kvh, hd.row0, hd.n};
             }
             fresh = began = true;
             if (r == n - 1) break;
             p.step = 0;  // on to the next unit
             if (++p.y == U) {
                 p.y = 0;
+#pragma unroll 1
                 do p.nt = bt.steps(++p.b);
                 while (p.nt == 0);
             }
@@ -617,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (lane <= kWarps) {
         int w0 = max(lane - 1, 0);
         if (lane == 0)
-            while (sm.empty[w0]) ++w0;  // some warp of a CTA with work has steps
+            while (w0 < kWarps - 1 && sm.empty[w0]) ++w0;
         tc = sm.cut[lane > 0][w0];
 #pragma unroll
         for (int k = 0; k < kWarps; ++k)

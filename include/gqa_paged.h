@@ -166,8 +166,8 @@ int gqa_pick_splits(int B, int Hk, int max_seq_len, int page_size, int kv_dtype)
  *              pages (np = ceil(seq_len / page_size)), merged with lse_combine on the
  *              same stream
  *              GQA_KV_FP4: 0 or GQA_SPLITS_BALANCED, which are the same schedule (any B);
- *              GQA_ERR_SPLITS for explicit counts.  B * Hq * ceil(pt_stride * page_size / 32)
- *              must fit an int32
+ *              GQA_ERR_SPLITS for explicit counts.  B * Hq * (ceil(pt_stride * page_size / 32)
+ *              + 1) must fit an int32
  *   pack_gqa   1 (default): all heads of a group in one thread block, each KV page read
  *              once; 0: one query head per thread block (for comparison sweeps only)
  *   out        bf16 [B][Hq][head_dim]
