@@ -431,6 +431,64 @@ def test_decode_of_many_sequences(B, per):
     close(out, lse, expect(c, q, scale))
 
 
+LARGE = [
+    # B, Hq, Hk, D, P, longest, share of empty sequences: several steps for every warp of the GPU
+    (128, 32, 8, 128, 16, 2500, 0.1),
+    (600, 32, 8, 128, 16, 700, 0.4),      # runs of sequences
+    (90, 56, 8, 64, 64, 4000, 0.0),
+    (48, 64, 4, 128, 32, 3000, 0.05),     # two blocks of heads
+    (3, 64, 8, 128, 64, 33000, 0.0),
+    (256, 8, 8, 128, 16, 1100, 0.9),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LARGE)))
+def test_decode_of_large_batches_is_the_bf16_decode_of_what_is_read_back(case):
+    """Code times scale is a bf16 value, so the cache read back is exact and the bf16 decode over it says the
+    same.  Both outputs are rounded to bf16 (2^-8 of each), the weights here are f16 (2^-11, and fp32 work of
+    2^-15) and there two bf16 terms (2^-15); a score error of 2^-17 scale sum |q| |k| on either side."""
+    B, Hq, Hk, D, P, most, none = LARGE[case]
+    r = rng(100 + case)
+    lens = r.integers(1, most + 1, B)
+    lens[r.uniform(size=B) < none] = 0
+    lens[-1] = max(lens[-1], 1)
+    need = (lens + P - 1) // P
+    pages = int(need.sum()) + 3
+    perm = r.permutation(pages).astype(np.int32)
+    table = np.full((B, max(1, int(need.max()))), -1, np.int32)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    gen = torch.Generator(DEV).manual_seed(case)
+    pools = []
+    for _ in range(2):
+        x = torch.randint(0, 256, (pages, Hk, P // 16, 9 * D), generator=gen, device=DEV, dtype=torch.uint8)
+        x[..., 8 * D:] = torch.randint(0x20, 0x39, x[..., 8 * D:].shape, generator=gen, device=DEV, dtype=torch.uint8)
+        pools.append(x.view(pages, Hk, P, 9 * D // 16))
+    table, sl = dev(table), dev(lens.astype(np.int32))
+    q = torch.randn(B, Hq, D, generator=gen, device=DEV).to(torch.bfloat16)
+    scale = 0.5 * D ** -0.5
+    ws = binding.new_workspace(16 << 20, DEV)
+    out, lse = binding.gqa_paged_decode(q, *pools, table, sl, scale, workspace=ws)
+    cu = cu_of(need, torch.int64)
+    kb, vb = binding.gqa_paged_read_kv(*pools, table, sl, cu, int(need.sum()), paged=True, workspace=ws,
+                                       k_out=torch.zeros(int(need.sum()), Hk, P, D, dtype=torch.bfloat16, device=DEV),
+                                       v_out=torch.zeros(int(need.sum()), Hk, P, D, dtype=torch.bfloat16, device=DEV))
+    assert binding.gqa_get_error(ws) == 0
+    cols = torch.arange(table.shape[1], device=DEV)
+    back = (cu[:-1, None] + cols).to(torch.int32).clamp(max=int(need.sum()) - 1).contiguous()
+    ref, lref = binding.gqa_paged_decode(q, kb, vb, back, sl, scale)
+    pv, _ = binding.gqa_paged_decode(q, kb, vb.abs(), back, sl, scale)
+    o, got, pv = ref.double(), out.double(), pv.double() * (1 + 2.0 ** -7)
+    e = 2 * 2.0 ** -17 * scale * (q.abs().double().sum(-1) * kb.abs().max().double())
+    tol = 2.0 ** -7 * o.abs() + (2.0 ** -11 + 2.0 ** -14 + 2 * e[..., None]) * pv + 1e-30
+    assert bool(((got - o).abs() <= tol).all()), float(((got - o).abs() / tol).max())
+    fin = torch.isfinite(lref)
+    assert torch.equal(fin, torch.isfinite(lse)) and torch.equal(fin, (sl > 0)[:, None].expand_as(fin))
+    assert bool(((lse - lref).abs() <= e.float() + 2.0 ** -18 + 2.0 ** -21 * lref.abs())[fin].all())
+
+
 def test_one_workspace_for_changing_batches():
     """Batch sizes and head counts in turn on one workspace that was zeroed once."""
     ws = binding.new_workspace(16 << 20, DEV)
