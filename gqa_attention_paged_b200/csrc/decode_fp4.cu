@@ -6,7 +6,8 @@
 // once; the softmax is the online form ("TensorRT-LLM与TensorRT核心差异解析", section 4.2.1).
 //
 // Schedule.  The 32-token steps of all (sequence, kv head [, block of heads]) units are laid end
-// to end and cut into equal contiguous shares, one per warp of a fixed grid.  Going on to a unit (its
+// to end and cut into equal contiguous shares, one per warp of a fixed grid (or, few and short, given
+// a CTA each).  Going on to a unit (its
 // q, the last one's results) takes as long as a step, so with several steps a warp a unit counts one
 // place more than its steps; without that, warps with many short units came last (64 sequences of
 // 0 .. 4096 tokens: 43.0 us, 38.5 with it).  A warp streams its share through a private shared-memory ring of 16-byte asynchronous copies (a tile's codes and
@@ -25,8 +26,8 @@
 //
 // What bounds it.  A step of 32 tokens is 561 instructions a warp, 128 conversions and 128 scale
 // multiplications among them, 96 us of arithmetic at 256 x 2048 tokens and 8 kv heads where the
-// copies alone take 98; together 112 us (607 MB, 5.4 TB/s), 128 once the power cap holds the clock.
-// 64 x 2048: 37 us, of which 3 go before the first keys and 4 into the merges; 1 x 2048: 10 us.
+// copies alone take 98; together 113 us (607 MB, 5.4 TB/s), 129 once the power cap holds the clock.
+// 64 x 2048: 37 us, of which 3 go before the first keys and 4 into the merges; 1 x 2048: 10.2 us.
 #include <atomic>
 
 #include "fp4.cuh"
@@ -52,6 +53,10 @@ constexpr int kStep = 2 * kFp4Tile;  // tokens of a step: two tiles
 // and with: 13 steps a warp 34.3 and 28.8, 7.1 30.5 and 26.9, 4.2 19.8 and 20.3, 2.0 14.9 and 15.3;
 // uniform ones 1% slower with it (64 x 2048: 36.9 and 37.1).
 constexpr int kWeighted = 5;
+// Steps of the longest unit up to which, when there are no more units than CTAs, each has a CTA of its
+// own and nothing is merged between CTAs (us, without and with: 8 units of 7 steps 9.5 and 5.8, of 22
+// 10.6 and 8.0, of 32 9.4 and 9.3, of 47 11.3 and 11.9; 288 units of 32 steps 17.7 and 14.2).
+constexpr int kWhole = 32;
 constexpr int kRuns = kThreads;      // the sequences' step prefix is kept per run of ceil(B / kRuns)
 
 template <int D>
@@ -483,15 +488,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
     // ---- steps before each run of sequences
     int none = 0;  // a sequence without tokens?
+    bool whole = bt.per == 1 && a.B * U <= (int)gridDim.x;  // few short units, a CTA each?
     {
         const int b0 = min(a.B, (int)threadIdx.x * bt.per), b1 = min(a.B, b0 + bt.per);
-        int incl = 0;
+        int incl = 0, longest = 0;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int L0 = __ldg(a.seq_lens + b), L = clamped(a, L0);
             if (L != L0 && blockIdx.x == 0) set_error(a.err, GQA_ERR_BAD_PAGE);
             if (bt.per == 1) sm.len[b] = L;
             incl += steps_of(L);
+            longest = steps_of(L);
             none |= L == 0;
         }
 #pragma unroll
@@ -506,6 +513,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         sm.pre[threadIdx.x + 1] = incl;
         if (threadIdx.x == 0) sm.pre[0] = 0;
         none = __syncthreads_or(none);
+        if (whole) whole = !__syncthreads_or(longest > kWhole);
     }
     const int total = U * sm.pre[kRuns];
     bt.more = weighted(total);
@@ -523,28 +531,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
         }
     }
-    // CTAs with work
-    const int NC = max(1, min((int)gridDim.x, T / kWarps));
-    if (T == 0 || blockIdx.x >= NC) return;
-
-    // ---- this warp's share: n steps from place s_w on
-    Shares sh;
-    // (below the whole grid NC is T / kWarps: a step each, and one more for some)
-    sh.q = NC == (int)gridDim.x ? (int)((unsigned)T / (gridDim.x * kWarps)) : (T >= kWarps ? 1 : 0);
-    sh.rem = T - sh.q * (NC * kWarps);
-    const int s_w = sh.start(blockIdx.x * kWarps + warp), e_w = sh.start(blockIdx.x * kWarps + warp + 1);
-    int n = e_w - s_w, index = 0;
+    // ---- this warp's share: n steps from p on
+    Shares sh = {0, 0};
     Pos p = {a.B - 1, 0, 0, 1};
-    if (n > 0) p = locate(s_w, bt, lane, index);
-    if (bt.more) {
-        int end = total;
-        if (e_w < T) locate(e_w, bt, lane, end);
-        n = end - index;
+    int n;
+    if (whole) {
+        // a CTA per unit
+        if (blockIdx.x >= a.B * U) return;
+        const int b = blockIdx.x / U, nt = bt.steps(b);
+        if (nt == 0) return;
+        const int from = nt * warp / kWarps;
+        n = nt * (warp + 1) / kWarps - from;
+        p = {b, (int)blockIdx.x - b * U, from, nt};
+    } else {
+        const int NC = max(1, min((int)gridDim.x, T / kWarps));  // CTAs with work
+        if (T == 0 || blockIdx.x >= NC) return;
+        // (below the whole grid NC is T / kWarps: a step each, and one more for some)
+        sh.q = NC == (int)gridDim.x ? (int)((unsigned)T / (gridDim.x * kWarps)) : (T >= kWarps ? 1 : 0);
+        sh.rem = T - sh.q * (NC * kWarps);
+        const int s_w = sh.start(blockIdx.x * kWarps + warp), e_w = sh.start(blockIdx.x * kWarps + warp + 1);
+        int index = 0;
+        n = e_w - s_w;
+        if (n > 0) p = locate(s_w, bt, lane, index);
+        if (bt.more) {
+            int end = total;
+            if (e_w < T) locate(e_w, bt, lane, end);
+            n = end - index;
+        }
     }
     if (lane < 2) sm.cut[lane][warp].unit = -1;
-    if (lane == 0) {
-        sm.empty[warp] = n == 0;
-    }
+    if (lane == 0) sm.empty[warp] = n == 0;
     __syncwarp();
     if (n > 0) {
         const uint64_t policy = policy_evict_first();
@@ -668,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         has |= 1u << w0;
     }
     // does the unit go on in other CTAs?  From which to which?
-    const bool cross = tc.unit >= 0 && (tc.first < c_start || tc.first + tc.steps > c_end);
+    const bool cross = !whole && tc.unit >= 0 && (tc.first < c_start || tc.first + tc.steps > c_end);
     const int c0 = cross ? sh.owner(tc.first) / kWarps : 0, c1 = cross ? sh.owner(tc.first + tc.steps - 1) / kWarps : 0;
     const unsigned crossing = __ballot_sync(kFull, cross);
     auto put = [&](int row, int kvh, const float(&acc)[V], float M, float L) {

@@ -392,6 +392,14 @@ CASES = [
     (12, 1, 128, 16, [400]),              # groups of 12
     (8, 1, 128, 16, [2100]),              # one long sequence
     (2, 1, 64, 16, [16] * 70 + [0] * 5 + [33] * 3),   # many short ones
+    # a sequence above 1024 tokens: the whole batch is cut into equal shares, units between CTAs
+    (8, 2, 64, 16, [37, 1100, 0, 1]),
+    (16, 1, 128, 16, [1300, 90, 31]),
+    (24, 1, 128, 32, [16, 0, 1100]),
+    (14, 2, 64, 32, [1200, 5]),
+    (4, 1, 128, 64, [0, 1030, 65, 64]),
+    (4, 2, 64, 16, [1025] * 3),
+    (4, 2, 64, 16, [1024, 1023, 993, 992, 33, 32]),   # 32 steps and just below: a CTA per unit
 ]
 
 
@@ -492,7 +500,7 @@ def test_decode_of_large_batches_is_the_bf16_decode_of_what_is_read_back(case):
 def test_one_workspace_for_changing_batches():
     """Batch sizes and head counts in turn on one workspace that was zeroed once."""
     ws = binding.new_workspace(16 << 20, DEV)
-    shapes = [([300], 8, 2, 128), ([200, 90, 310] * 4, 8, 2, 128), ([700], 16, 1, 64), ([5] * 40 + [400], 4, 2, 128)]
+    shapes = [([1300], 8, 2, 128), ([200, 90, 310] * 4, 8, 2, 128), ([1700], 16, 1, 64), ([5] * 40 + [1400], 4, 2, 128)]
     batches = []
     for i, (lens, Hq, Hk, D) in enumerate(shapes):
         c = Cache(lens, Hk, D, 16, seed=70 + i).fill()
@@ -507,7 +515,7 @@ def test_one_workspace_for_changing_batches():
 
 def test_two_decodes_at_once():
     """Two streams, a workspace each."""
-    c = Cache([900, 300], 2, 128, 16, seed=81).fill()
+    c = Cache([1100, 300], 2, 128, 16, seed=81).fill()
     d, ref = c.to_gpu(), None
     q = queries(c, 2, 8)
     ref, qd = expect(c, q, 0.1), q.to(DEV)
@@ -735,12 +743,13 @@ def test_compiled_calls_take_valid_tensors_only():
 
 # ----------------------------------------------------------------------- streams, graphs, all together
 
-def test_decode_in_a_graph_and_on_another_stream():
-    c = Cache([90, 0, 260, 16], 2, 128, 16, seed=31).fill()
+@pytest.mark.parametrize("lens", [[90, 0, 260, 16], [90, 0, 1060, 16]])
+def test_decode_in_a_graph_and_on_another_stream(lens):
+    c = Cache(lens, 2, 128, 16, seed=31).fill()
     q, scale = queries(c, 4, 16).to(DEV), 0.09
     ref = expect(c, q.cpu(), scale)
     d = c.to_gpu()
-    ws = binding.new_workspace(binding.gqa_paged_decode_workspace_size(4, 16, 2, 128, 16, 272, 2, 0), DEV)
+    ws = binding.new_workspace(binding.gqa_paged_decode_workspace_size(4, 16, 2, 128, 16, 1072, 2, 0), DEV)
     out, lse = torch.zeros(4, 16, 128, dtype=torch.bfloat16, device=DEV), torch.zeros(4, 16, device=DEV)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
