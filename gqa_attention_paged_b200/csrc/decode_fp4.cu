@@ -6,16 +6,16 @@
 // once; the softmax is the online form ("TensorRT-LLM与TensorRT核心差异解析", section 4.2.1).
 //
 // Schedule.  The 32-token steps of all (sequence, kv head [, block of heads]) units are laid end
-// to end and cut into equal contiguous shares, one per warp of a fixed grid (or, few and short, given
-// a CTA each).  Going on to a unit (its
-// q, the last one's results) takes as long as a step, so with several steps a warp a unit counts one
-// place more than its steps; without that, warps with many short units came last (64 sequences of
-// 0 .. 4096 tokens: 43.0 us, 38.5 with it).  A warp streams its share through a private shared-memory ring of 16-byte asynchronous copies (a tile's codes and
-// scales are contiguous; a bulk copy per tile, 1152 bytes, was bound by the copies an SM can
-// start, about one in 32 cycles): the step is taken into registers and its slot handed to the step
-// kStages further on.  No warp waits for another until the end.  Units cut between the warps of a
-// CTA are then merged through shared memory; those cut between CTAs leave one piece per CTA in the
-// workspace, and the last CTA to arrive merges them, in the order of the CTAs.
+// to end and cut into equal contiguous shares, one per warp of a fixed grid; units that are few and
+// short have a CTA each instead.  Going on to a unit (its q, the last one's results) takes as long as
+// a step, so with several steps a warp a unit counts one place more than its steps; without that,
+// warps with many short units came last (64 sequences of 0 .. 4096 tokens: 43.0 us, 38.5 with it).
+// A warp streams its share through a private shared-memory ring of 16-byte asynchronous copies (a
+// tile's codes and scales are contiguous; a bulk copy per tile, 1152 bytes, was bound by the copies
+// an SM can start, about one in 32 cycles): the step is taken into registers and its slot handed to
+// the step kStages further on.  No warp waits for another until the end.  Units cut between the warps
+// of a CTA are then merged through shared memory; those cut between CTAs leave one piece per CTA in
+// the workspace, and the last CTA to arrive merges them, in the order of the CTAs.
 //
 // Tile.  S^T = K q^T and O^T += V^T P^T on m16n8k16 f16 tensor-core fragments: tokens (dims) are M,
 // 8 packed heads N.  The operands code * scale are exact f16 values; q is bf16 scaled per head by
@@ -99,7 +99,7 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Not volatile: the products of a step's scores and of the step before run in one another's gaps.
+// Not volatile, so that the compiler may move them (64 x 2048: 39.4 -> 38.7 us).
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
