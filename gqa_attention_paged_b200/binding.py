@@ -254,7 +254,10 @@ def gqa_paged_prefill_workspace_size(total_q, Hq, head_dim) -> int:
 
 
 def new_workspace(nbytes: int, device) -> torch.Tensor:
-    """A zero-filled, 256-byte aligned workspace of at least nbytes."""
+    """A zero-filled, 256-byte aligned workspace of at least nbytes.  One of them serves calls of
+    every kind in turn on a stream, but for the balanced bf16 / e4m3 decode, which counts behind the
+    header: give it one of its own, or zero it after a prefill, a sparse selection, a split decode or a
+    balanced decode of fewer rows (include/gqa_paged.h)."""
     n = (max(int(nbytes), 256) + 255) // 256 * 256
     return torch.zeros(n, dtype=torch.uint8, device=device)
 

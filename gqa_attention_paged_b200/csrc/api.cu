@@ -249,8 +249,10 @@ int decode_call(const void *q, const void *k_pages, const void *v_pages, const f
         f.out_f32 = out_f32;
         f.lse = lse;
         f.err = reinterpret_cast<int *>(ws);
-        f.counters = reinterpret_cast<int *>(ws + kWorkspaceHeader);
-        f.pieces = reinterpret_cast<float *>(ws + fp4_decode_zero_bytes());
+        f.arrivals = reinterpret_cast<unsigned *>(ws) + 1;
+        // against the workspace's end: the other pools' decode keeps counters that have to stay zero at
+        // the front, and with the same heads its own pieces are larger than these
+        f.pieces = reinterpret_cast<float *>(ws + (workspace_bytes - fp4_decode_piece_bytes(Hq, Hk, head_dim)) / 256 * 256);
         f.sms = sm_count() > kStreamMaxSms ? kStreamMaxSms : sm_count();
         return launch_decode_fp4(f, stream) == cudaSuccess ? GQA_OK : GQA_ERR_LAUNCH;
     }
@@ -334,7 +336,7 @@ size_t gqa_paged_decode_workspace_size(int B, int Hq, int Hk, int head_dim, int 
     if (kv_dtype == GQA_KV_FP4)
         return B < 0 || Hq <= 0 || Hk <= 0 || Hq % Hk != 0
                    ? kWorkspaceHeader
-                   : fp4_decode_zero_bytes() + fp4_decode_piece_bytes(Hq, Hk, head_dim);
+                   : kWorkspaceHeader + fp4_decode_piece_bytes(Hq, Hk, head_dim);
     const int S = decode_schedule(num_splits, B, Hk, max_seq_len, page_size, kv_dtype);
     if (S == 0 && Hq > 0 && Hk > 0 && Hq % Hk == 0)
         return decode_zero_prefix_bytes(B, Hq) + stream_k_piece_bytes(Hq, Hk, head_dim);

@@ -58,6 +58,32 @@ constexpr int kWeighted = 5;
 // 10.6 and 8.0, of 32 9.4 and 9.3, of 47 11.3 and 11.9; 288 units of 32 steps 17.7 and 14.2).
 constexpr int kWhole = 32;
 constexpr int kRuns = kThreads;      // the sequences' step prefix is kept per run of ceil(B / kRuns)
+constexpr int kMaxCtas = kStreamMaxSms * kCtasPerSm;
+constexpr int kPieceLine = 32;       // floats: a piece begins on a line of 128 bytes
+
+__host__ __device__ constexpr int piece_floats(int heads, int D) {
+    return (heads * (D + 2) + kPieceLine - 1) / kPieceLine * kPieceLine;
+}
+
+// The count of a unit's CTAs that have left their pieces.  It lies in the workspace's header, behind the
+// error word, where no call of the library keeps scratch, so that a zeroed workspace serves calls of any
+// kind in turn.  That is room for 5 bits a CTA, six fields a word.  A unit from CTA c0 to c1 counts in
+// c0's field, which is its alone because no other such unit begins in c0; if 5 bits are too few, the unit
+// covers the 11 CTAs behind c0, in whose fields no other unit counts, and with them the next whole word.
+struct Arrivals {
+    static constexpr int kBits = 5, kFields = 32 / kBits;
+    static constexpr int kWords = (kMaxCtas - 1) / kFields + 2;
+    int word, shift;
+    unsigned mask;
+    __device__ __forceinline__ Arrivals(int c0, int c1) {
+        const bool small = c1 - c0 + 1 < 1 << kBits;
+        word = c0 / kFields + (small ? 0 : 1);
+        shift = small ? c0 % kFields * kBits : 0;
+        mask = small ? (1u << kBits) - 1 : ~0u;
+    }
+};
+static_assert(sizeof(int) * (1 + Arrivals::kWords) <= kWorkspaceHeader, "the counts fit the header");
+static_assert((1 << Arrivals::kBits) > 2 * Arrivals::kFields, "a unit that needs a word covers one");
 
 template <int D>
 struct Cfg {
@@ -670,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // the unit that an earlier CTA began.  Its states lie in warp order.  Lane t looks task t up; a
     // warp then merges one head of one task at a time, each lane D / 32 dims.
     const int c_start = sh.start(blockIdx.x * kWarps), c_end = sh.start((blockIdx.x + 1) * kWarps);
-    const int slot_floats = hpc * (D + 2);
+    const int slot_floats = piece_floats(hpc, D);
     Cut tc = {-1, 0, 0, 0, 0, 0};
     unsigned has = 0;  // the warps that have a state of it
     if (lane <= kWarps) {
@@ -734,12 +760,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // arrive merges the pieces
     __syncthreads();
     if (warp == 0 && cross) {
-        // one counter per CTA that such a unit begins in: no CTA has two
         // (release: the CTA's pieces, by way of the barrier; acquire: those of the CTAs before)
-        int before;
-        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(a.counters + c0) : "memory");
-        const bool last = before == c1 - c0;
-        if (last) a.counters[c0] = 0;  // ready for the next launch
+        const Arrivals at(c0, c1);
+        unsigned *count = a.arrivals + at.word, before;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(before) : "l"(count), "r"(1u << at.shift) : "memory");
+        const bool last = (before >> at.shift & at.mask) == (unsigned)(c1 - c0);
+        if (last) atomicSub(count, (unsigned)(c1 - c0 + 1) << at.shift);  // zero again for the next launch
         sm.last[lane > 0] = last ? c1 - c0 + 1 : 0;
     }
     __syncthreads();
@@ -815,14 +841,10 @@ cudaError_t launch_t(const Fp4DecodeArgs &a, cudaStream_t stream) {
 
 }  // namespace
 
-// A counter per CTA of the largest grid, at a place that no batch size or head count moves: a
-// workspace that was zeroed once serves them all.
-size_t fp4_decode_zero_bytes() { return kWorkspaceHeader + (size_t)kStreamMaxSms * kCtasPerSm * sizeof(int); }
-
-// Two pieces per CTA.
+// Two pieces per CTA of the largest grid.
 size_t fp4_decode_piece_bytes(int Hq, int Hk, int D) {
     const int g = Hq / Hk, hpc = g < kHeads ? g : kHeads;
-    return (size_t)kStreamMaxSms * kCtasPerSm * 2 * hpc * (D + 2) * sizeof(float);
+    return (size_t)kMaxCtas * 2 * piece_floats(hpc, D) * sizeof(float);
 }
 
 cudaError_t launch_decode_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {

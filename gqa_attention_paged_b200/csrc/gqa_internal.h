@@ -9,7 +9,9 @@
 
 namespace gqa {
 
-constexpr size_t kWorkspaceHeader = 256;  // bytes before any scratch: holds the error word
+// Bytes before any scratch: the error word, then the 4-bit decode's counts of arrivals, which are zero
+// between launches.
+constexpr size_t kWorkspaceHeader = 256;
 
 struct DecodeArgs {
     const void *q;

@@ -60,12 +60,11 @@ struct Fp4DecodeArgs {
     int out_f32;
     float *lse;
     int *err;
-    int *counters;  // one per CTA, zero between launches
+    unsigned *arrivals;  // of a cut unit's pieces, in the workspace's header; zero between launches
     float *pieces;
     int sms;
 };
-size_t fp4_decode_zero_bytes();  // the error word and the counters
-size_t fp4_decode_piece_bytes(int Hq, int Hk, int D);
+size_t fp4_decode_piece_bytes(int Hq, int Hk, int D);  // a multiple of 256
 cudaError_t launch_decode_fp4(const Fp4DecodeArgs &a, cudaStream_t stream);
 
 }  // namespace gqa

@@ -12,7 +12,6 @@
 #include <mutex>
 
 #include "gqa_internal.h"
-#include "quant_kv.h"
 #include "gqa_paged.h"
 
 namespace {
@@ -63,9 +62,9 @@ extern "C" int gqa_paged_decode_static_scratch(
     const int st = scratch_address(&ws);
     if (st != GQA_OK) return st;
     // The array keeps the previous call's contents.  What must start at zero is cleared:
-    // the error word and the balanced schedule's merge counters (split partials and merge
+    // the header and the balanced schedule's merge counters (split partials and merge
     // pieces are fully rewritten by every call that reads them).
-    size_t zero = kv_dtype == GQA_KV_FP4 ? gqa::fp4_decode_zero_bytes() : gqa::decode_zero_prefix_bytes(B, Hq);
+    size_t zero = kv_dtype == GQA_KV_FP4 ? gqa::kWorkspaceHeader : gqa::decode_zero_prefix_bytes(B, Hq);
     if (zero > (size_t)GQA_STATIC_SCRATCH_BYTES) zero = (size_t)GQA_STATIC_SCRATCH_BYTES;
     if (cudaMemsetAsync(ws, 0, zero, stream) != cudaSuccess) return GQA_ERR_LAUNCH;
     return gqa_paged_decode(q, k_pages, v_pages, k_scale, v_scale, kv_dtype, page_table,

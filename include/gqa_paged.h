@@ -34,6 +34,16 @@
  *     and cleared by gqa_get_error().  A workspace must be zero-filled once before its
  *     first use; after that the library only ever sets the word and gqa_get_error()
  *     clears it.
+ *   - The first 256 bytes of a workspace are its header (the error word, and counts that are
+ *     zero between launches); what follows is scratch.  One workspace, large enough for each,
+ *     serves calls of every kind in turn on a stream, with one exception: the balanced
+ *     schedule of bf16 and e4m3 decode (the sparse decode's too) counts in the first B*Hq int32
+ *     behind the header, which have to be zero when it is called.  It leaves them zero, and the
+ *     appends, writes, read backs and 4-bit decodes do not touch them (the last of the same
+ *     heads, or if the workspace has room for both behind one another); a prefill, a sparse
+ *     selection, a split decode and a balanced decode of fewer rows write there.  Give that
+ *     decode a workspace of its own, or zero it in between.
+ *   - Calls that may run at the same time (other streams) need a workspace each.
  *   - Layouts are row-major (C order).  KV pools are [num_pages][Hk][page_size][head_dim]
  *     ("HND": each (page, kv head) block is one contiguous run).  q and out are bf16.
  *   - Sequence lengths count the current token(s): the new K/V are in the cache, written
@@ -104,10 +114,9 @@ typedef enum {
  * Bytes of workspace gqa_paged_decode() needs for the same B, heads, head_dim, page_size,
  * longest context (pt_stride * page_size), kv_dtype and num_splits.  Layout: a 256-byte
  * header holding the device error word, then
- *   GQA_KV_FP4: int32 merge counters [160 SMs x 2 CTAs] and the merge pieces, 2 per CTA, each
- *     min(Hq/Hk, 8) x (head_dim + 2) fp32.  The counters' place depends on nothing, so that a
- *     workspace zeroed once and large enough serves any batch size and head count; one that
- *     served other pools' decode calls is zeroed before;
+ *   GQA_KV_FP4: the merge pieces, 2 per CTA (160 SMs x 2 CTAs), each min(Hq/Hk, 8) x
+ *     (head_dim + 2) fp32 rounded up to 128 bytes, at the end of the workspace (their arrivals
+ *     are counted in the header);
  *   num_splits = 0, B <= 2048 (balanced schedule): int32 merge counters [B*Hq] (rounded
  *     up to 256 bytes) and the merge pieces, 2 per worker of the largest grid
  *     (160 SMs x 2 CTAs x 4 workers), each min(Hq/Hk, 16) x (head_dim + 1) fp32;
