@@ -139,6 +139,30 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _made(stream, make) -> torch.Tensor:
+    """A buffer that a call makes for itself: of the stream that the call runs on, so that its zeros are
+    there before the kernels and its memory is not reused before they are done."""
+    if stream is None:
+        return make()
+    now = torch.cuda.current_stream()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    if stream.cuda_stream == now.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(now)  # (the caller may use and free it there)
+    return t
+
+
+def _empty(stream, shape, dtype, device) -> torch.Tensor:
+    return _made(stream, lambda: torch.empty(shape, dtype=dtype, device=device))
+
+
+def _scratch(stream, nbytes: int, device) -> torch.Tensor:
+    return _made(stream, lambda: new_workspace(nbytes, device))
+
+
 def _fast_call(fn: str, name: str, args, stream) -> bool:
     """Call `fn` of the compiled half: True if it was done.  False, with nothing done, for tensors
     that are not all as the function wants them: the caller's own checks then say what is wrong
@@ -295,14 +319,14 @@ def gqa_paged_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale, here)
     pt_stride = page_table.shape[1]
     if out is None:
-        out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, Hq, D), torch.bfloat16, q.device)
     _need(out, "out", torch.bfloat16, (B, Hq, D), here)
     if lse is None and want_lse:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (B, Hq), torch.float32, q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, Hq), here)
     if workspace is None:  # (a given one's size is checked by the call)
-        workspace = new_workspace(gqa_paged_decode_workspace_size(
+        workspace = _scratch(stream, gqa_paged_decode_workspace_size(
             B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits), q.device)
     _need(workspace, "workspace", torch.uint8, None, here)
     st = load().gqa_paged_decode(
@@ -347,13 +371,13 @@ def gqa_paged_decode_partial(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
     _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale, here)
     pt_stride = page_table.shape[1]
     if o_part is None:
-        o_part = torch.empty(B, Hq, D, dtype=torch.float32, device=q.device)
+        o_part = _empty(stream, (B, Hq, D), torch.float32, q.device)
     _need(o_part, "o_part", torch.float32, (B, Hq, D), here)
     if lse_part is None:
-        lse_part = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        lse_part = _empty(stream, (B, Hq), torch.float32, q.device)
     _need(lse_part, "lse_part", torch.float32, (B, Hq), here)
     if workspace is None:  # (a given one's size is checked by the call)
-        workspace = new_workspace(gqa_paged_decode_workspace_size(
+        workspace = _scratch(stream, gqa_paged_decode_workspace_size(
             B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits), q.device)
     _need(workspace, "workspace", torch.uint8, None, here)
     st = load().gqa_paged_decode_partial(
@@ -391,9 +415,9 @@ def gqa_paged_decode_static_scratch(q: torch.Tensor, k_pages: torch.Tensor,
     if kv_dtype == GQA_KV_FP4:
         _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale, here)
     if out is None:
-        out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, Hq, D), torch.bfloat16, q.device)
     if lse is None:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (B, Hq), torch.float32, q.device)
     _need(out, "out", torch.bfloat16, (B, Hq, D), here)
     _need(lse, "lse", torch.float32, (B, Hq), here)
     st = load().gqa_paged_decode_static_scratch(
@@ -438,7 +462,7 @@ def gqa_paged_append_kv(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch
     B, Hk, D, P, num_pages, kv_dtype, here = _append_args(
         k_new, v_new, k_pages, v_pages, page_table, seq_lens, k_scale, v_scale)
     if workspace is None:
-        workspace = new_workspace(256, k_pages.device)
+        workspace = _scratch(stream, 256, k_pages.device)
     if kv_dtype == GQA_KV_FP4:
         _need_word(here, workspace)
     _need(workspace, "workspace", torch.uint8)
@@ -473,14 +497,14 @@ def gqa_paged_append_decode(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.T
         raise ValueError("q must be [B][Hq][head_dim] with the pools' head_dim")
     pt_stride = page_table.shape[1]
     if out is None:
-        out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, Hq, D), torch.bfloat16, q.device)
     _need(out, "out", torch.bfloat16, (B, Hq, D), here)
     if lse is None and want_lse:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (B, Hq), torch.float32, q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, Hq), here)
     if workspace is None:  # (a given one's size is checked by the call)
-        workspace = new_workspace(gqa_paged_decode_workspace_size(
+        workspace = _scratch(stream, gqa_paged_decode_workspace_size(
             B, Hq, Hk, D, P, pt_stride * P, kv_dtype, num_splits), q.device)
     _need(workspace, "workspace", torch.uint8, None, here)
     st = load().gqa_paged_append_decode(
@@ -512,14 +536,14 @@ def gqa_paged_prefill(q: torch.Tensor, cu_q: torch.Tensor, k_pages: torch.Tensor
     _need(seq_lens, "seq_lens", torch.int32, (B,))
     pt_stride = page_table.shape[1]
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (T, Hq, D), torch.bfloat16, q.device)
     _need(out, "out", torch.bfloat16, (T, Hq, D))
     if lse is None and want_lse:
-        lse = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (T, Hq), torch.float32, q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, (T, Hq))
     if workspace is None:
-        workspace = new_workspace(gqa_paged_prefill_workspace_size(T, Hq, D), q.device)
+        workspace = _scratch(stream, gqa_paged_prefill_workspace_size(T, Hq, D), q.device)
     st = load().gqa_paged_prefill(
         _ptr(q), _ptr(cu_q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), pt_stride,
         _ptr(seq_lens), B, Hq, Hk, D, P, num_pages, float(scale), int(bool(causal)), T,
@@ -537,10 +561,10 @@ def lse_combine(o_part: torch.Tensor, lse_part: torch.Tensor,
     S, rows, D = o_part.shape
     _need(lse_part, "lse_part", torch.float32, (S, rows))
     if out is None:
-        out = torch.empty(rows, D, dtype=torch.bfloat16, device=o_part.device)
+        out = _empty(stream, (rows, D), torch.bfloat16, o_part.device)
     _need(out, "out", torch.bfloat16, (rows, D))
     if lse is None:
-        lse = torch.empty(rows, dtype=torch.float32, device=o_part.device)
+        lse = _empty(stream, rows, torch.float32, o_part.device)
     _need(lse, "lse", torch.float32, (rows,))
     st = load().lse_combine(_ptr(o_part), _ptr(lse_part), S, rows, D, _ptr(out), _ptr(lse),
                             _stream(stream))
@@ -616,7 +640,7 @@ def gqa_paged_write_kv(k_new: torch.Tensor, v_new: torch.Tensor, cu_q: torch.Ten
     _need(cu_q, "cu_q", torch.int32, (B + 1,), here)
     pt_stride = _table_on(here, page_table, B)
     if workspace is None:
-        workspace = new_workspace(256, k_pages.device)
+        workspace = _scratch(stream, 256, k_pages.device)
     _need_word(here, workspace)
     if T == 0:
         return workspace
@@ -657,13 +681,13 @@ def gqa_paged_read_kv(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: 
     total = int(total)
     shape = (total, Hk, P, D) if paged else (total, Hk, D)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+        k_out = _empty(stream, shape, torch.bfloat16, k_pages.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=k_pages.device)
+        v_out = _empty(stream, shape, torch.bfloat16, k_pages.device)
     _need(k_out, "k_out", torch.bfloat16, shape, here)
     _need(v_out, "v_out", torch.bfloat16, shape, here)
     if workspace is None:
-        workspace = new_workspace(256, k_pages.device)
+        workspace = _scratch(stream, 256, k_pages.device)
     _need_word(here, workspace)
     if total == 0:
         return k_out, v_out
@@ -686,8 +710,8 @@ def gqa_paged_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: t
     _need(page_table, "page_table", torch.int32)
     _need(seq_lens, "seq_lens", torch.int32, (B,))
     _need(cu_kv, "cu_kv", torch.int64, (B + 1,))
-    ko = torch.empty(total, Hk, D, dtype=k_pages.dtype, device=k_pages.device)
-    vo = torch.empty_like(ko)
+    ko = _empty(stream, (total, Hk, D), k_pages.dtype, k_pages.device)
+    vo = _empty(stream, (total, Hk, D), k_pages.dtype, k_pages.device)
     st = load().gqa_paged_gather(_ptr(k_pages), _ptr(v_pages), _ptr(page_table),
                                  page_table.shape[1], _ptr(seq_lens), _ptr(cu_kv), B, Hk, D, P,
                                  num_pages, k_pages.element_size(), _ptr(ko), _ptr(vo),
@@ -735,10 +759,10 @@ def gqa_paged_kt_build(k_pages: torch.Tensor, page_table: torch.Tensor, seq_lens
     _need(seq_lens, "seq_lens", torch.int32)
     B = seq_lens.shape[0]
     if kt is None:
-        kt = new_kt_cache(k_pages)
+        kt = _made(stream, lambda: new_kt_cache(k_pages))
     _need(kt, "kt", torch.bfloat16, (num_pages, Hk, D, 2))
     if workspace is None:
-        workspace = new_workspace(256, k_pages.device)
+        workspace = _scratch(stream, 256, k_pages.device)
     st = load().gqa_paged_kt_build(_ptr(k_pages), _ptr(page_table), page_table.shape[1],
                                    _ptr(seq_lens), B, Hk, D, P, num_pages, _ptr(kt),
                                    _ptr(workspace), _stream(stream))
@@ -758,7 +782,7 @@ def gqa_paged_kt_append(k_new: torch.Tensor, page_table: torch.Tensor, seq_lens:
     _need(page_table, "page_table", torch.int32)
     _need(seq_lens, "seq_lens", torch.int32, (B,))
     if workspace is None:
-        workspace = new_workspace(256, kt.device)
+        workspace = _scratch(stream, 256, kt.device)
     st = load().gqa_paged_kt_append(_ptr(k_new), _ptr(page_table), page_table.shape[1],
                                     _ptr(seq_lens), B, Hk, D, int(page_size), num_pages, _ptr(kt),
                                     _ptr(workspace), _stream(stream))
@@ -780,11 +804,11 @@ def gqa_paged_sparse_select(q: torch.Tensor, kt: torch.Tensor, k_pages: torch.Te
     _need(kt, "kt", torch.bfloat16, (num_pages, Hk, D, 2))
     ss = gqa_paged_sparse_table_stride(pts, P, topk, window)
     dev = q.device
-    sel_table = torch.full((B * Hk, max(ss, 1)), -1, dtype=torch.int32, device=dev)
-    sel_pages = torch.full((B * Hk, max(ss, 1)), -1, dtype=torch.int32, device=dev)
-    sel_lens = torch.zeros(B * Hk, dtype=torch.int32, device=dev)
+    sel_table = _made(stream, lambda: torch.full((B * Hk, max(ss, 1)), -1, dtype=torch.int32, device=dev))
+    sel_pages = _made(stream, lambda: torch.full((B * Hk, max(ss, 1)), -1, dtype=torch.int32, device=dev))
+    sel_lens = _made(stream, lambda: torch.zeros(B * Hk, dtype=torch.int32, device=dev))
     if workspace is None:
-        workspace = new_workspace(load().gqa_paged_sparse_select_workspace_size(B, Hk, pts), dev)
+        workspace = _scratch(stream, load().gqa_paged_sparse_select_workspace_size(B, Hk, pts), dev)
     st = load().gqa_paged_sparse_select(_ptr(q), _ptr(kt), _ptr(page_table), pts, _ptr(seq_lens),
                                         B, Hq, Hk, D, P, num_pages, int(topk), int(window),
                                         _ptr(sel_table), max(ss, 1), _ptr(sel_lens),
@@ -812,15 +836,15 @@ def gqa_paged_sparse_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
     _need(v_pages, "v_pages", torch.bfloat16, k_pages.shape)
     _need(kt, "kt", torch.bfloat16, (num_pages, Hk, D, 2))
     if out is None:
-        out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=q.device)
+        out = _empty(stream, (B, Hq, D), torch.bfloat16, q.device)
     _need(out, "out", torch.bfloat16, (B, Hq, D))
     if lse is None and want_lse:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        lse = _empty(stream, (B, Hq), torch.float32, q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, Hq))
     need = gqa_paged_sparse_decode_workspace_size(B, Hq, Hk, D, P, pts, topk, window, num_splits)
     if workspace is None:
-        workspace = new_workspace(need, q.device)
+        workspace = _scratch(stream, need, q.device)
     _need(workspace, "workspace", torch.uint8)
     st = load().gqa_paged_sparse_decode(
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(kt), _ptr(page_table), pts, _ptr(seq_lens),
