@@ -412,8 +412,9 @@ def gqa_paged_decode_static_scratch(q: torch.Tensor, k_pages: torch.Tensor,
         raise ValueError("head_dim of q and the KV pools differ")
     _need(page_table, "page_table", torch.int32, None, here)
     _need(seq_lens, "seq_lens", torch.int32, (B,), here)
-    if kv_dtype == GQA_KV_FP4:
-        _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale, here)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [B][pt_stride]")
+    _need_scales(kv_dtype, num_pages, Hk, k_scale, v_scale, here)
     if out is None:
         out = _empty(stream, (B, Hq, D), torch.bfloat16, q.device)
     if lse is None:
