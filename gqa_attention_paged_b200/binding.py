@@ -533,9 +533,8 @@ def gqa_paged_prefill(q: torch.Tensor, cu_q: torch.Tensor, k_pages: torch.Tensor
         raise ValueError("head_dim of q and the KV pools differ")
     B = seq_lens.shape[0]
     _need(cu_q, "cu_q", torch.int32, (B + 1,))
-    _need(page_table, "page_table", torch.int32)
+    pt_stride = _table_on(None, page_table, B)
     _need(seq_lens, "seq_lens", torch.int32, (B,))
-    pt_stride = page_table.shape[1]
     if out is None:
         out = _empty(stream, (T, Hq, D), torch.bfloat16, q.device)
     _need(out, "out", torch.bfloat16, (T, Hq, D))
@@ -610,7 +609,7 @@ def _pools_on(here: int, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale, 
     return kv_dtype, D, num_pages, Hk, P
 
 
-def _table_on(here: int, page_table: torch.Tensor, B: int) -> int:
+def _table_on(here: Optional[int], page_table: torch.Tensor, B: int) -> int:
     _need(page_table, "page_table", torch.int32, None, here)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [B][pt_stride]")
@@ -708,13 +707,13 @@ def gqa_paged_gather(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: t
     _need(v_pages, "v_pages", k_pages.dtype, k_pages.shape)
     num_pages, Hk, P, D = k_pages.shape
     B = seq_lens.shape[0]
-    _need(page_table, "page_table", torch.int32)
+    pt_stride = _table_on(None, page_table, B)
     _need(seq_lens, "seq_lens", torch.int32, (B,))
     _need(cu_kv, "cu_kv", torch.int64, (B + 1,))
     ko = _empty(stream, (total, Hk, D), k_pages.dtype, k_pages.device)
     vo = _empty(stream, (total, Hk, D), k_pages.dtype, k_pages.device)
     st = load().gqa_paged_gather(_ptr(k_pages), _ptr(v_pages), _ptr(page_table),
-                                 page_table.shape[1], _ptr(seq_lens), _ptr(cu_kv), B, Hk, D, P,
+                                 pt_stride, _ptr(seq_lens), _ptr(cu_kv), B, Hk, D, P,
                                  num_pages, k_pages.element_size(), _ptr(ko), _ptr(vo),
                                  _stream(stream))
     _check("gqa_paged_gather", st)
@@ -756,15 +755,15 @@ def gqa_paged_kt_build(k_pages: torch.Tensor, page_table: torch.Tensor, seq_lens
     of every page the sequences reference; returns kt bf16 [num_pages][Hk][D][2]."""
     _need(k_pages, "k_pages", torch.bfloat16)
     num_pages, Hk, P, D = k_pages.shape
-    _need(page_table, "page_table", torch.int32)
     _need(seq_lens, "seq_lens", torch.int32)
     B = seq_lens.shape[0]
+    pt_stride = _table_on(None, page_table, B)
     if kt is None:
         kt = _made(stream, lambda: new_kt_cache(k_pages))
     _need(kt, "kt", torch.bfloat16, (num_pages, Hk, D, 2))
     if workspace is None:
         workspace = _scratch(stream, 256, k_pages.device)
-    st = load().gqa_paged_kt_build(_ptr(k_pages), _ptr(page_table), page_table.shape[1],
+    st = load().gqa_paged_kt_build(_ptr(k_pages), _ptr(page_table), pt_stride,
                                    _ptr(seq_lens), B, Hk, D, P, num_pages, _ptr(kt),
                                    _ptr(workspace), _stream(stream))
     _check("gqa_paged_kt_build", st)
@@ -778,13 +777,13 @@ def gqa_paged_kt_append(k_new: torch.Tensor, page_table: torch.Tensor, seq_lens:
     [B][Hk][D]), in place."""
     _need(k_new, "k_new", torch.bfloat16)
     B, Hk, D = k_new.shape
-    _need(kt, "kt", torch.bfloat16)
     num_pages = kt.shape[0]
-    _need(page_table, "page_table", torch.int32)
+    _need(kt, "kt", torch.bfloat16, (num_pages, Hk, D, 2))
+    pt_stride = _table_on(None, page_table, B)
     _need(seq_lens, "seq_lens", torch.int32, (B,))
     if workspace is None:
         workspace = _scratch(stream, 256, kt.device)
-    st = load().gqa_paged_kt_append(_ptr(k_new), _ptr(page_table), page_table.shape[1],
+    st = load().gqa_paged_kt_append(_ptr(k_new), _ptr(page_table), pt_stride,
                                     _ptr(seq_lens), B, Hk, D, int(page_size), num_pages, _ptr(kt),
                                     _ptr(workspace), _stream(stream))
     _check("gqa_paged_kt_append", st)
