@@ -29,6 +29,7 @@ GQA_SPLITS_BALANCED = -1
 
 _lib = None
 _fast = None
+_fast_off = None  # why there is no compiled half
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
@@ -101,11 +102,19 @@ def load(path: Optional[str] = None):
 
 
 def _load_fastcall(lib):
-    """The compiled half of the hottest functions below (csrc/fastcall.cpp), on this library."""
-    global _fast
-    loader = importlib.machinery.ExtensionFileLoader("_fastcall", _build.FASTCALL)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fastcall", loader))
-    loader.exec_module(module)
+    """The compiled half of the hottest functions below (csrc/fastcall.cpp), on this library.  Where it
+    cannot be built or loaded, their Python half makes every call."""
+    global _fast, _fast_off
+    _fast, _fast_off = None, _build.build_fastcall() if _build._fastcall_stale() else None
+    if _fast_off is not None:
+        return
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("_fastcall", _build.FASTCALL)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fastcall", loader))
+        loader.exec_module(module)
+    except ImportError as e:
+        _fast_off = str(e)
+        return
     module.init(torch.Tensor,
                 *(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
                     "gqa_paged_decode", "gqa_paged_decode_partial", "gqa_paged_append_kv",
@@ -167,8 +176,10 @@ def _fast_call(fn: str, name: str, args, stream) -> bool:
     """Call `fn` of the compiled half: True if it was done.  False, with nothing done, for tensors
     that are not all as the function wants them: the caller's own checks then say what is wrong
     (or make the call, on tensors that only Python looks through)."""
-    if _fast is None:
+    if _lib is None:
         load()
+    if _fast is None:
+        return False
     try:
         here = _get_device()
     except (RuntimeError, AssertionError):  # no GPU
