@@ -541,6 +541,7 @@ int gqa_paged_write_kv(const void *k_new, const void *v_new, int64_t k_stride, i
         (int64_t)num_pages * Hk * page_size > INT32_MAX ||
         (int64_t)pt_stride * page_size > INT32_MAX || k_stride < (int64_t)Hk * head_dim ||
         v_stride < (int64_t)Hk * head_dim ||
+        // (2^43 elements at most, as in gqa_paged_read_kv)
         ((int64_t)total_q * Hk * (head_dim / 16) + 255) / 256 > INT32_MAX)
         return GQA_ERR_SHAPE;
     if (!aligned(k_new, 16) || !aligned(v_new, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
@@ -587,7 +588,8 @@ int gqa_paged_read_kv(const void *k_pages, const void *v_pages, const float *k_s
         !valid_page_size(page_size) || num_pages <= 0 || pt_stride <= 0 || total < 0 ||
         total > INT32_MAX || (int64_t)num_pages * Hk * page_size > INT32_MAX ||
         (int64_t)pt_stride * page_size > INT32_MAX ||
-        // a thread per (row, kv head, 16 dims) in blocks of 256
+        // 2^43 elements at most, 16 TiB of each output: a CTA takes 16 rows or more and 128 (row, kv
+        // head) pairs or more of them, so that the grid and 16-row groups stay far inside their types
         total * (paged ? page_size : 1) > ((int64_t)INT32_MAX * 256) / ((int64_t)Hk * (head_dim / 16)))
         return GQA_ERR_SHAPE;
     if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_out, 16) ||

@@ -30,12 +30,6 @@ constexpr int kFp4Tile = 16;  // tokens of a tile
 
 __host__ __device__ constexpr int fp4_tile_bytes(int D) { return 9 * D; }
 
-// Byte offset of tile `slot / 16` of a (page, kv head) block; num_pages * Hk * P fits an int32,
-// the byte offset does not.
-__host__ __device__ inline size_t fp4_tile_offset(int phys, int Hk, int kvh, int P, int slot, int D) {
-    return (((size_t)phys * Hk + kvh) * (size_t)(P / kFp4Tile) + (size_t)(slot / kFp4Tile)) * (size_t)fp4_tile_bytes(D);
-}
-
 // Two codes of a byte (low nibble first) -> f16x2, exact.
 __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
