@@ -9,9 +9,7 @@
 
 namespace gqa {
 
-// Bytes before any scratch: the error word, then the 4-bit decode's counts of arrivals, which are zero
-// between launches.
-constexpr size_t kWorkspaceHeader = 256;
+constexpr size_t kWorkspaceHeader = 256;  // bytes before any scratch: holds the error word
 
 struct DecodeArgs {
     const void *q;
