@@ -24,10 +24,11 @@
 // running sum are fp32.  Groups above 8 run as blocks of 8 heads, whose second read of a tile is an
 // L2 hit (groups of 16, 48 x 0 .. 3000 tokens: 26.8 us; one block of 16 heads took 5 more).
 //
-// What bounds it.  A step of 32 tokens is 561 instructions a warp, 128 conversions and 128 scale
-// multiplications among them, 96 us of arithmetic at 256 x 2048 tokens and 8 kv heads where the
-// copies alone take 98; together 113 us (607 MB, 5.4 TB/s), 129 once the power cap holds the clock.
-// 64 x 2048: 37 us, of which 3 go before the first keys and 4 into the merges; 1 x 2048: 10.2 us.
+// What bounds it.  At 64 x 2048 tokens and 8 kv heads a step of 32 tokens comes to 645 instructions a
+// warp with all that is around it, 128 conversions and 128 scale multiplications among them.  Issue is
+// active 56% of the time and no pipe above 46%: it is the latency of a step's chain at 15 warps an SM.
+// 37 us there, of which 3 go before the first keys and 4 into the merges; 1 x 2048: 10.2 us; 256 x 2048:
+// 112 us (607 MB, 5.4 TB/s; copies alone 98), 129 once the power cap holds the clock.
 #include <atomic>
 
 #include "fp4.cuh"
@@ -51,7 +52,7 @@ constexpr float kNoRef = -3e38f;  // below every reference
 constexpr int kStep = 2 * kFp4Tile;  // tokens of a step: two tiles
 // Steps a warp from which on a unit counts one place more than its steps.  Ragged lengths, us without
 // and with: 13 steps a warp 34.3 and 28.8, 7.1 30.5 and 26.9, 4.2 19.8 and 20.3, 2.0 14.9 and 15.3;
-// uniform ones 1% slower with it (64 x 2048: 36.9 and 37.1).
+// uniform ones 1 to 3% slower with it (64 x 2048: 36.9 and 37.1, 256 x 2048: 109 and 112).
 constexpr int kWeighted = 5;
 // Steps of the longest unit up to which, when there are no more units than CTAs, each has a CTA of its
 // own and nothing is merged between CTAs (us, without and with: 8 units of 7 steps 9.5 and 5.8, of 22
@@ -391,7 +392,7 @@ struct State {
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[h][e] = fmaf(s[h][e], kmul[e & 1], -m[e & 1]);
         if (valid < kStep) {  // what follows the sequence may be anything: its scores and scales go
-            __syncwarp();     // (keeps this a branch: 113 -> 109.5 us at batch 256)
+            __syncwarp();     // (keeps this a branch: 113 -> 109.5 us at batch 256, before a unit had an extra place)
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
                 if (2 * cq + 8 * h >= valid) vs[h] = 0u;

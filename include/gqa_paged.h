@@ -211,7 +211,9 @@ int gqa_paged_decode(const void *q, const void *k_pages, const void *v_pages,
  * sequence, 0 for a sequence with none here).  The results are written in fp32 instead of
  * bf16, in the form lse_combine() takes for one split:
  *   o_part    fp32 [B][Hq][head_dim]: softmax-normalised attention over the covered tokens
- *             (0 for a sequence with none), 16-byte aligned
+ *             (0 for a sequence with none), 16-byte aligned.  Its error is that of the weights
+ *             in the product with V: 4-bit and e4m3 pools round each to f16 (2^-11), bf16 pools
+ *             to two bf16 terms (2^-16); their sum, and all other sums, are fp32
  *   lse_part  fp32 [B][Hq]: natural-log log-sum-exp of the covered scores (-inf for a
  *             sequence with none); required (NULL gives GQA_ERR_NULL)
  * Stacking the o_part / lse_part of R such calls (R ranks, or R disjoint page ranges) as
