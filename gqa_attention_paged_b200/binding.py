@@ -534,7 +534,8 @@ def gqa_paged_prefill(q: torch.Tensor, cu_q: torch.Tensor, k_pages: torch.Tensor
                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                       workspace: Optional[torch.Tensor] = None, want_lse: bool = True,
                       stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
-    """Causal chunked prefill.  q bf16 [total_q][Hq][D]; cu_q int32 [B+1]; bf16 pools."""
+    """Causal chunked prefill.  q bf16 [total_q][Hq][D]; cu_q int32 [B+1]; bf16 pools.  A workspace
+    that a balanced bf16 / e4m3 decode uses too is zeroed in between (new_workspace)."""
     _need(q, "q", torch.bfloat16)
     T, Hq, D = q.shape
     _need(k_pages, "k_pages", torch.bfloat16)
@@ -810,7 +811,8 @@ def gqa_paged_sparse_select(q: torch.Tensor, kt: torch.Tensor, k_pages: torch.Te
                             window: int, workspace: Optional[torch.Tensor] = None,
                             stream=None):
     """The chosen pages: returns (sel_table int32 [B*Hk][ss] of physical*Hk + kv head,
-    sel_lens int32 [B*Hk], sel_pages int32 [B*Hk][ss] logical pages)."""
+    sel_lens int32 [B*Hk], sel_pages int32 [B*Hk][ss] logical pages).  A workspace that a balanced
+    bf16 / e4m3 decode uses too is zeroed in between (new_workspace)."""
     B, Hq, Hk, D, P, num_pages, pts = _sparse_common(q, k_pages, page_table, seq_lens)
     _need(kt, "kt", torch.bfloat16, (num_pages, Hk, D, 2))
     ss = gqa_paged_sparse_table_stride(pts, P, topk, window)
@@ -842,7 +844,8 @@ def gqa_paged_sparse_decode(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
                             workspace: Optional[torch.Tensor] = None, want_lse: bool = True,
                             stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Page-level top-K sparse decode (bf16 pools): the window pages plus the topk
-    best-scoring earlier pages of every (sequence, kv head) are attended."""
+    best-scoring earlier pages of every (sequence, kv head) are attended.  The workspace holds a
+    balanced decode's counters (new_workspace)."""
     B, Hq, Hk, D, P, num_pages, pts = _sparse_common(q, k_pages, page_table, seq_lens)
     _need(v_pages, "v_pages", torch.bfloat16, k_pages.shape)
     _need(kt, "kt", torch.bfloat16, (num_pages, Hk, D, 2))

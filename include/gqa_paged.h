@@ -183,8 +183,9 @@ int gqa_pick_splits(int B, int Hk, int max_seq_len, int page_size, int kv_dtype)
  *   lse        fp32 [B][Hq] natural-log log-sum-exp, or NULL
  *   workspace  >= gqa_paged_decode_workspace_size(...) bytes, 256-byte aligned, zeroed
  *              before first use.  The balanced schedule keeps one merge counter per
- *              (sequence, head) in it, back to zero at the end of every launch; after a
- *              device-side error (see gqa_get_error) zero the workspace again.
+ *              (sequence, head) in it, back to zero at the end of every launch: of the
+ *              calls that share the workspace (conventions above) some write there; after
+ *              a device-side error (see gqa_get_error) zero the workspace again.
  * The balanced schedule's kernel is launched with programmatic stream serialization: its
  * CTAs may start (shared-memory set-up only) while the previous kernel on `stream` is
  * still running, and read or write no global memory until that kernel has completed.
@@ -300,7 +301,8 @@ size_t gqa_paged_prefill_workspace_size(int total_q, int Hq, int head_dim);
  *   k_pages, v_pages, page_table, pt_stride, seq_lens: as for decode (bf16 KV only)
  *   head_dim   64 or 128; page_size in {16, 32, 64}; Hq / Hk <= 128; scale > 0
  *   out        bf16 [total_q][Hq][head_dim];  lse fp32 [total_q][Hq] or NULL
- *   workspace  >= gqa_paged_prefill_workspace_size(...) bytes, zeroed before first use
+ *   workspace  >= gqa_paged_prefill_workspace_size(...) bytes, zeroed before first use;
+ *              it writes over the counters of a balanced bf16 / e4m3 decode on the same one
  */
 int gqa_paged_prefill(const void *q, const int32_t *cu_q, const void *k_pages,
                       const void *v_pages, const int32_t *page_table, int pt_stride,
@@ -502,7 +504,8 @@ size_t gqa_paged_sparse_select_workspace_size(int B, int Hk, int pt_stride);
  *   sel_stride >= gqa_paged_sparse_table_stride(pt_stride, page_size, topk, window)
  * workspace: >= gqa_paged_sparse_select_workspace_size(B, Hk, pt_stride) bytes, 256-byte
  * aligned, zeroed before first use (error word, then the scores between the two kernels:
- * one scores pages in chunks of 64 over a (chunk, kv head, sequence) grid, one picks).
+ * one scores pages in chunks of 64 over a (chunk, kv head, sequence) grid, one picks).  The
+ * scores lie over the counters of a balanced bf16 / e4m3 decode on the same workspace.
  */
 int gqa_paged_sparse_select(const void *q, const void *kt, const int32_t *page_table,
                             int pt_stride, const int32_t *seq_lens, int B, int Hq, int Hk,
@@ -523,7 +526,8 @@ size_t gqa_paged_sparse_decode_workspace_size(int B, int Hq, int Hk, int head_di
  * (bf16 pools), except that num_splits = 0 runs the balanced schedule for the decode of the
  * chosen pages (measured faster on the 70B shape than the split count the decode table
  * gives for that size); kt as for gqa_paged_kt_build(); B * Hk <= 65535.  The workspace holds the
- * chosen-page table between the two kernels; zero it once before first use.
+ * chosen-page table between the two kernels; zero it once before first use.  Its decode counts in
+ * it like gqa_paged_decode()'s balanced schedule.
  */
 int gqa_paged_sparse_decode(const void *q, const void *k_pages, const void *v_pages,
                             const void *kt, const int32_t *page_table, int pt_stride,
